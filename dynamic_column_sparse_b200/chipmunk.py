@@ -14,6 +14,10 @@ Layouts (all tensors on the same CUDA device, contiguous):
   y_cache [T][D] fp32, out [T][D] bf16.
 * Attention: q, k, v [T][h][128] bf16, idx [h][nb][k] int32, m_c, l_c [h][T]
   fp32, acc_c [h][T][128] fp32, o [T][h][128] bf16.
+* Around them: 4-bit microscaled rows (``Fp4Rows``), ``linear_fp4`` x [T][K] or
+  quantised, w [N][K] quantised, ``norm_residual`` res, y [T][D] with gate, scale,
+  shift [B][D] (row-strided views of one projection are fine), ``qk_norm_rope``
+  qkv [T][>= 3 h 128] (row-strided) to q, k, v [T][h][128].
 """
 from __future__ import annotations
 
@@ -29,7 +33,7 @@ LIB_PATH = os.path.join(_HERE, "libchipmunk.so")
 
 OK = 0
 ERR_INVALID_ARG, ERR_SHAPE, ERR_ALIGNMENT, ERR_CUDA, ERR_DEVICE, ERR_UNSUPPORTED, ERR_WORKSPACE = 1, 2, 3, 4, 5, 6, 7
-OP_TOPK, OP_MLP_DELTA, OP_ATTN_DELTA, OP_REFRESH, OP_MLP_DELTA_FP8 = 0, 1, 2, 3, 4
+OP_TOPK, OP_MLP_DELTA, OP_ATTN_DELTA, OP_REFRESH, OP_MLP_DELTA_FP8, OP_LINEAR_FP4 = 0, 1, 2, 3, 4, 5
 REFRESH_MLP, REFRESH_ATTN = 0, 1
 
 EXPORTS = (
@@ -38,6 +42,8 @@ EXPORTS = (
     "chipmunk_gather_cols", "chipmunk_scatter_cols", "chipmunk_workspace_bytes", "chipmunk_status_string",
     "chipmunk_last_error", "chipmunk_read_device_status", "chipmunk_version", "chipmunk_mlp_delta_noalloc",
     "chipmunk_selftest_bounded_wait", "chipmunk_mlp_delta_fp8", "chipmunk_quantize_e4m3_rows",
+    "chipmunk_fp4_scale_bytes", "chipmunk_quantize_fp4_rows", "chipmunk_dequantize_fp4_rows", "chipmunk_linear_fp4",
+    "chipmunk_norm_residual", "chipmunk_qk_norm_rope",
 )
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -86,6 +92,43 @@ class RefreshArgs(ctypes.Structure):
     ]
 
 
+class Fp4Args(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("format", ctypes.c_int32),
+        ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("row_scales", ctypes.c_void_p),
+    ]
+
+
+class LinearFp4Args(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("N", ctypes.c_int64), ("act", ctypes.c_int32), ("out_type", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("xq", Fp4Args), ("w", Fp4Args), ("bias", ctypes.c_void_p), ("out", ctypes.c_void_p),
+    ]
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("D", ctypes.c_int64), ("B", ctypes.c_int64),
+        ("res_type", ctypes.c_int32), ("y_type", ctypes.c_int32), ("mod_type", ctypes.c_int32),
+        ("post_norm", ctypes.c_int32), ("norm", ctypes.c_int32), ("out_format", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("res_scale", ctypes.c_float),
+        ("res", ctypes.c_void_p), ("y", ctypes.c_void_p), ("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+        ("res_out", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p), ("ld_mod", ctypes.c_int64),
+        ("offsets", ctypes.c_void_p), ("out", ctypes.c_void_p), ("out_scales", ctypes.c_void_p),
+        ("out_row_scales", ctypes.c_void_p),
+    ]
+
+
+class HeadsArgs(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("ld", ctypes.c_int64), ("h", ctypes.c_int32), ("pairs", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("qkv", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -114,6 +157,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "chipmunk_selftest_bounded_wait": [vp],
             "chipmunk_mlp_delta_fp8": [ctypes.POINTER(MlpFp8Args), vp, sz, vp],
             "chipmunk_quantize_e4m3_rows": [vp, i64, i64, vp, vp, vp],
+            "chipmunk_quantize_fp4_rows": [vp, ctypes.POINTER(Fp4Args), vp],
+            "chipmunk_dequantize_fp4_rows": [ctypes.POINTER(Fp4Args), i32, vp, vp],
+            "chipmunk_linear_fp4": [ctypes.POINTER(LinearFp4Args), vp, sz, vp],
+            "chipmunk_norm_residual": [ctypes.POINTER(NormArgs), vp],
+            "chipmunk_qk_norm_rope": [ctypes.POINTER(HeadsArgs), vp],
         }
         for name, argtypes in sig.items():
             fn = getattr(lib, name)
@@ -121,6 +169,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             fn.restype = i32
         lib.chipmunk_workspace_bytes.argtypes = [i32, vp]
         lib.chipmunk_workspace_bytes.restype = sz
+        lib.chipmunk_fp4_scale_bytes.argtypes = [i64, i64, i32]
+        lib.chipmunk_fp4_scale_bytes.restype = sz
         lib.chipmunk_status_string.argtypes = [i32]
         lib.chipmunk_status_string.restype = ctypes.c_char_p
         lib.chipmunk_last_error.argtypes = []
@@ -426,3 +476,285 @@ def scatter_cols(packed, idx, a_cache, stream=None):
     _need(packed, "packed", torch.bfloat16, (nb, k, Bt))
     _check(lib.chipmunk_scatter_cols(_ptr(packed), nb, H, Bt, _ptr(idx), k, _ptr(a_cache), _stream(stream)))
     return a_cache
+
+
+# ------------------------------------------------------------------ around the sparse layers
+
+NVFP4, MXFP4 = 0, 1
+_FP4_FORMATS = {"nvfp4": NVFP4, "mxfp4": MXFP4}
+_ACTS = {"none": 0, "gelu": 1}
+_NORMS = {"none": 0, "layer": 1, "rms": 2}
+_NORM_OUT = {"bf16": 0, "e4m3": 1, "nvfp4": 2, "mxfp4": 3}
+_PAIRS = {"interleaved": 0, "halves": 1}
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _pick(table, key, name):
+    try:
+        return table[key]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name} must be one of {', '.join(map(str, table))}, got {key!r}") from None
+
+
+def _here(t, name, dtypes, shape, dev):
+    """A contiguous CUDA tensor of one of ``dtypes`` and of ``shape``, on ``dev``."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be on {dev if dev.type == 'cuda' else 'a CUDA device'}, is on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_U8 = (torch.uint8,)
+_I32 = (torch.int32,)
+_BF16_F32 = (torch.bfloat16, torch.float32)
+
+
+def _empty(shape, dtype, dev, stream):
+    """Uninitialised device memory that belongs to the stream that will use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _call(dev, stream, fn, *args):
+    """Runs a C entry point (stream last) with ``dev`` current, on ``stream`` or dev's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, stream.cuda_stream))
+
+
+class Fp4Rows:
+    """Rows of 4-bit microscaled values: ``codes`` uint8 [rows][cols / 2] (lower column in the low
+    nibble), ``scales`` uint8 (block scales in the tensor core's order, ``fp4_scale_bytes`` of
+    them), ``row_scales`` fp32 [rows] (nvfp4; None for mxfp4). The header of the C ABI defines both
+    formats and the order of the scales."""
+
+    __slots__ = ("codes", "scales", "row_scales", "fmt", "rows", "cols", "args")
+
+    def __init__(self, codes, scales, row_scales, fmt, rows, cols):
+        f = _pick(_FP4_FORMATS, fmt, "fmt")
+        need = fp4_scale_bytes(rows, cols, fmt)
+        dev = getattr(codes, "device", None)
+        _here(codes, "codes", _U8, (rows, cols // 2), dev)
+        if not isinstance(scales, torch.Tensor) or scales.numel() != need:
+            raise ValueError(f"scales must hold {need} bytes")
+        _here(scales, "scales", _U8, scales.shape, dev)
+        if f == NVFP4:
+            _here(row_scales, "row_scales", _F32, (rows,), dev)
+        elif row_scales is not None:
+            raise ValueError("mxfp4 rows have no row scales")
+        self.codes, self.scales, self.row_scales = codes, scales, row_scales
+        self.fmt, self.rows, self.cols = fmt, rows, cols
+        self.args = Fp4Args(rows, cols, f, codes.data_ptr(), scales.data_ptr(),
+                            None if row_scales is None else row_scales.data_ptr())
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def fp4_scale_bytes(rows: int, cols: int, fmt: str) -> int:
+    """Bytes of the block scales of rows x cols 4-bit values."""
+    if not 0 <= rows <= 1 << 30 or not 32 <= cols <= 65536 or cols % 32:
+        raise ValueError(f"{rows} rows x {cols} columns: columns must be a multiple of 32 in [32, 65536]")
+    return int(load_library().chipmunk_fp4_scale_bytes(rows, cols, _pick(_FP4_FORMATS, fmt, "fmt")))
+
+
+def empty_fp4_rows(rows: int, cols: int, fmt: str, device, stream=None) -> Fp4Rows:
+    """Uninitialised 4-bit rows for a quantising call to fill."""
+    dev = torch.device(device)
+    n = fp4_scale_bytes(rows, cols, fmt)
+    return Fp4Rows(_empty((rows, cols // 2), torch.uint8, dev, stream), _empty((n,), torch.uint8, dev, stream),
+                   _empty((rows,), torch.float32, dev, stream) if fmt == "nvfp4" else None, fmt, rows, cols)
+
+
+def quantize_fp4_rows(x, fmt="nvfp4", out: Fp4Rows | None = None, stream=None) -> Fp4Rows:
+    """Rows of bf16 x [R][C] to 4-bit microscaled rows (C a multiple of 32)."""
+    lib = load_library()
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor")
+    R, C = x.shape
+    _here(x, "x", _BF16, (R, C), x.device)
+    if out is None:
+        out = empty_fp4_rows(R, C, fmt, x.device, stream)
+    elif (out.rows, out.cols, out.fmt) != (R, C, fmt) or out.device != x.device:
+        raise ValueError(f"out holds {out.rows} x {out.cols} {out.fmt} on {out.device}, x needs {R} x {C} {fmt}")
+    _call(x.device, stream, lib.chipmunk_quantize_fp4_rows, x.data_ptr(), ctypes.byref(out.args))
+    return out
+
+
+def dequantize_fp4_rows(q: Fp4Rows, out=None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values that 4-bit rows stand for, [R][C] in bf16 (exact) or fp32."""
+    lib = load_library()
+    if out is None:
+        out = _empty((q.rows, q.cols), dtype, q.device, stream)
+    _here(out, "out", _BF16_F32, (q.rows, q.cols), q.device)
+    _call(q.device, stream, lib.chipmunk_dequantize_fp4_rows, ctypes.byref(q.args), _TYPES[out.dtype], out.data_ptr())
+    return out
+
+
+def linear_fp4_workspace_bytes(T: int, K: int, fmt: str) -> int:
+    """Workspace of a linear_fp4 call that quantises its x (none for quantised x)."""
+    w = Fp4Args(8, K, _pick(_FP4_FORMATS, fmt, "fmt"), 16, 16, 16)
+    return workspace_bytes(OP_LINEAR_FP4, LinearFp4Args(T, 8, 0, 0, 16, Fp4Args(), w, None, None))
+
+
+def linear_fp4(x, w: Fp4Rows, bias=None, out=None, act="none", out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """act(x w^T + bias) on 4-bit operands: x bf16 [T][K] (quantised inside, into ``workspace``) or
+    Fp4Rows [T][K], w Fp4Rows [N][K], bias bf16 [N], out [T][N] bf16 or fp32. Calls that run at
+    the same time, captured ones included, must not share a workspace."""
+    lib = load_library()
+    dev, N, K = w.device, w.rows, w.cols
+    a = LinearFp4Args()
+    if isinstance(x, Fp4Rows):
+        T = x.rows
+        if x.cols != K or x.fmt != w.fmt or x.device != dev:
+            raise ValueError(f"x holds {x.cols} columns of {x.fmt} on {x.device}, w {K} of {w.fmt} on {dev}")
+        a.xq = x.args
+        need = 0
+    else:
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x must be a 2-D tensor or Fp4Rows")
+        T = x.shape[0]
+        _here(x, "x", _BF16, (T, K), dev)
+        a.x = x.data_ptr()
+        need = -1
+    if bias is not None:
+        _here(bias, "bias", _BF16, (N,), dev)
+        a.bias = bias.data_ptr()
+    if out is None:
+        out = _empty((T, N), out_dtype, dev, stream)
+    _here(out, "out", _BF16_F32, (T, N), dev)
+    a.T, a.N, a.act, a.out_type = T, N, _pick(_ACTS, act, "act"), _TYPES[out.dtype]
+    a.w, a.out = w.args, out.data_ptr()
+    ws_bytes = 0
+    if need:
+        if workspace is None:
+            workspace = _empty((workspace_bytes(OP_LINEAR_FP4, a),), torch.uint8, dev, stream)
+        elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _call(dev, stream, lib.chipmunk_linear_fp4, ctypes.byref(a), workspace.data_ptr() if need else None, ws_bytes)
+    return out
+
+
+def norm_residual(res, y=None, *, gate=None, post_norm="none", post_weight=None, res_scale=1.0, res_out=None,
+                  norm="layer", weight=None, bias=None, scale=None, shift=None, offsets=None, eps=1e-6, out=None,
+                  out_format="bf16", stream=None):
+    """r = res_scale * res + gate * post(y); h = (pre(r) * weight + bias) * (1 + scale) + shift.
+
+    res [T][D] and y [T][D] bf16 or fp32; gate, scale, shift [B][D] of one type (bf16 or fp32), row
+    strides allowed; offsets int32 [B + 1] on the device (rows outside it are left as they were) or
+    None for one sample. Returns (res_out, h): res_out is written when it is given (``res`` itself
+    updates in place) or when y is; h is bf16, (e4m3 codes, row scales) or Fp4Rows as out_format
+    says, into ``out`` when given, or None for out_format=None."""
+    lib = load_library()
+    if not isinstance(res, torch.Tensor) or res.dim() != 2:
+        raise ValueError("res must be a 2-D tensor")
+    T, D = res.shape
+    dev = res.device
+    a = NormArgs()
+    _here(res, "res", _BF16_F32, (T, D), dev)
+    a.T, a.D, a.res, a.res_type = T, D, res.data_ptr(), _TYPES[res.dtype]
+    a.post_norm, a.norm = _pick(_NORMS, post_norm, "post_norm"), _pick(_NORMS, norm, "norm")
+    a.eps, a.res_scale = eps, res_scale
+    if y is not None:
+        _here(y, "y", _BF16_F32, (T, D), dev)
+        a.y, a.y_type = y.data_ptr(), _TYPES[y.dtype]
+        if res_out is None:
+            res_out = _empty((T, D), res.dtype, dev, stream)
+    if res_out is not None:
+        _here(res_out, "res_out", (res.dtype,), (T, D), dev)
+        a.res_out = res_out.data_ptr()
+    for name, t in (("post_weight", post_weight), ("weight", weight), ("bias", bias)):
+        if t is not None:
+            _here(t, name, _BF16, (D,), dev)
+            setattr(a, name, t.data_ptr())
+    B = 1
+    if offsets is not None:
+        B = offsets.numel() - 1
+        if B < 1:
+            raise ValueError("offsets must hold at least two values")
+        _here(offsets, "offsets", _I32, (B + 1,), dev)
+        a.offsets = offsets.data_ptr()
+    a.B = B
+    mod_type = ld = None
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype not in _BF16_F32 or t.dtype != (mod_type or t.dtype):
+            raise TypeError("gate, scale and shift must be tensors of one type, bfloat16 or float32")
+        if t.device != dev or t.shape != (B, D) or t.stride(1) != 1:
+            raise ValueError(f"{name} must be [{B}][{D}] on {dev} with consecutive columns, is {tuple(t.shape)} on {t.device}")
+        row = t.stride(0) if B > 1 else D
+        if ld is not None and row != ld:
+            raise ValueError("gate, scale and shift must have the same row stride")
+        mod_type, ld = t.dtype, row
+        setattr(a, name, t.data_ptr())
+    if ld is not None:
+        a.mod_type, a.ld_mod = _TYPES[mod_type], ld
+    h = None
+    if out_format is not None:
+        f = a.out_format = _pick(_NORM_OUT, out_format, "out_format")
+        if f == 0:
+            h = _empty((T, D), torch.bfloat16, dev, stream) if out is None else out
+            _here(h, "out", _BF16, (T, D), dev)
+            a.out = h.data_ptr()
+        elif f == 1:
+            h = (_empty((T, D), torch.uint8, dev, stream), _empty((T,), torch.float32, dev, stream)) if out is None else out
+            _need_codes(h[0], "out codes", (T, D))
+            _here(h[1], "out scales", _F32, (T,), dev)
+            if h[0].device != dev:
+                raise ValueError(f"out codes must be on {dev}")
+            a.out, a.out_row_scales = h[0].data_ptr(), h[1].data_ptr()
+        else:
+            h = empty_fp4_rows(T, D, out_format, dev, stream) if out is None else out
+            if not isinstance(h, Fp4Rows) or (h.rows, h.cols, h.fmt) != (T, D, out_format) or h.device != dev:
+                raise ValueError(f"out must be Fp4Rows of {T} x {D} {out_format} on {dev}")
+            a.out, a.out_scales, a.out_row_scales = h.args.codes, h.args.scales, h.args.row_scales
+    _call(dev, stream, lib.chipmunk_norm_residual, ctypes.byref(a))
+    return res_out, h
+
+
+def qk_norm_rope(qkv, h, q_weight, k_weight, cos, sin, pairs="interleaved", eps=1e-6, q=None, k=None, v=None,
+                 stream=None):
+    """Heads out of a fused projection: qkv bf16 [T][>= 3 h 128] (rows may be strided), RMS norm of each
+    q and k head with q_weight, k_weight bf16 [128], rotation by cos, sin fp32 [T][64]; returns q, k,
+    v bf16 [T][h][128]."""
+    lib = load_library()
+    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 2:
+        raise ValueError("qkv must be a 2-D tensor")
+    T, C = qkv.shape
+    dev = qkv.device
+    if qkv.dtype != torch.bfloat16:
+        raise TypeError(f"qkv must be torch.bfloat16, got {qkv.dtype}")
+    if not qkv.is_cuda or qkv.stride(1) != 1 or C < 3 * h * 128:
+        raise ValueError(f"qkv must be a CUDA tensor with consecutive columns, at least {3 * h * 128}, has shape {tuple(qkv.shape)}")
+    _here(q_weight, "q_weight", _BF16, (128,), dev)
+    _here(k_weight, "k_weight", _BF16, (128,), dev)
+    _here(cos, "cos", _F32, (T, 64), dev)
+    _here(sin, "sin", _F32, (T, 64), dev)
+    shape = (T, h, 128)
+    q, k, v = (_empty(shape, torch.bfloat16, dev, stream) if t is None else t for t in (q, k, v))
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _here(t, name, _BF16, shape, dev)
+    a = HeadsArgs(T, qkv.stride(0) if T > 1 else 3 * h * 128, h, _pick(_PAIRS, pairs, "pairs"), eps, qkv.data_ptr(),
+                  q_weight.data_ptr(), k_weight.data_ptr(), cos.data_ptr(), sin.data_ptr(), q.data_ptr(), k.data_ptr(),
+                  v.data_ptr())
+    _call(dev, stream, lib.chipmunk_qk_norm_rope, ctypes.byref(a))
+    return q, k, v

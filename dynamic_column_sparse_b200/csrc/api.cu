@@ -16,6 +16,7 @@
 #include "ptx.cuh"
 
 namespace cm {
+size_t linear_fp4_ws(const chipmunk_linear_fp4_args *a);
 uint32_t attn_smem_bytes(int mode, int64_t T);
 }
 
@@ -284,6 +285,28 @@ namespace cm {
 
 chipmunk_status record_error(chipmunk_status st, const char *msg) { return fail(st, "%s", msg); }
 
+chipmunk_status record_errorf(chipmunk_status st, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(st, "%s", buf);
+}
+
+chipmunk_status device_ready(int **status_out) { return device_setup(status_out); }
+
+chipmunk_status encode_map2d(CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t rows, uint64_t cols,
+                             uint64_t pitch, uint32_t box_cols, uint32_t box_rows, const char *what) {
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
+  const cuuint32_t box[2] = {box_cols, box_rows}, es[2] = {1, 1};
+  CUresult r = g_encode(m, type, 2, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(CHIPMUNK_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, int(r));
+  return CHIPMUNK_OK;
+}
+
 chipmunk_status mlp_delta_fixed_scratch(const chipmunk_mlp_args *a, size_t scratch_bytes,
                                         chipmunk_status (*get_scratch)(void **), cudaStream_t s) {
   CM_CHECK(check_mlp(a, false));
@@ -329,6 +352,8 @@ size_t chipmunk_workspace_bytes(int32_t op, const void *args) {
       return args ? mlp_delta_ws(static_cast<const chipmunk_mlp_args *>(args)) : 0;
     case CHIPMUNK_OP_MLP_DELTA_FP8:
       return args ? mlp_delta_fp8_ws(static_cast<const chipmunk_mlp_fp8_args *>(args)) : 0;
+    case CHIPMUNK_OP_LINEAR_FP4:
+      return args ? cm::linear_fp4_ws(static_cast<const chipmunk_linear_fp4_args *>(args)) : 0;
     case CHIPMUNK_OP_REFRESH: {
       if (!args) return 0;
       const chipmunk_refresh_args *r = static_cast<const chipmunk_refresh_args *>(args);

@@ -1,0 +1,120 @@
+// fp4.cuh - 4-bit microscaled rows: formats, scale layout and the device
+// conversions shared by the quantiser and by the kernels that write quantised
+// rows themselves.
+//
+// A value is code * block scale (* row scale). Codes are e2m1 (magnitudes 0,
+// 0.5, 1, 1.5, 2, 3, 4, 6), two to a byte, the lower column in the low nibble.
+//   NVFP4: blocks of 16 columns, block scale e4m3, and a power-of-two fp32 row
+//          scale rs = 2^(floor(log2 max|row|) - 10), exponent clamped to
+//          [-110, 117] (1 for an all-zero row, NaN for a row that is not finite):
+//          block scale = e4m3(max|block| / (6 rs)), code = e2m1(x / (block scale * rs)).
+//   MXFP4: blocks of 32 columns, block scale 2^(floor(log2 max|block|) - 2) as
+//          an e8m0 byte (0 where the exponent would be below -127, 255 = NaN
+//          for a block that is not finite), code = e2m1(x / block scale).
+// Every rounding is to nearest, ties to even, saturating at the largest code.
+// bf16 inputs and power-of-two row scales make each quotient's distance from a
+// rounding border either zero or at least 2^-10 (see e2m1_grid), so fp32
+// arithmetic gives exactly the codes that exact arithmetic gives.
+//
+// Block scales lie in the order the tensor core's scale copies read: tiles of
+// 128 rows x 4 blocks, 512 bytes each, byte (r % 32) * 16 + (r % 128) / 32 * 4 +
+// block % 4; the tiles of 128 rows follow one another along the columns, padded
+// to a whole number of 256 columns.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "ptx.cuh"
+
+namespace cm {
+
+enum Fp4Format : int { kNvfp4 = 0, kMxfp4 = 1 };
+
+__host__ __device__ constexpr int fp4_block(int fmt) { return fmt == kNvfp4 ? 16 : 32; }
+// 512-byte scale tiles along the columns of 128 rows
+__host__ __device__ constexpr int64_t fp4_scale_tiles(int64_t cols, int fmt) {
+  return (cols + 255) / 256 * (fmt == kNvfp4 ? 4 : 2);
+}
+__host__ __device__ constexpr size_t fp4_scale_bytes(int64_t rows, int64_t cols, int fmt) {
+  return static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>(fp4_scale_tiles(cols, fmt)) * 512;
+}
+// Byte offset of the scale of (row, block): blocks 4i .. 4i+3 of a row are one aligned 4-byte word.
+__host__ __device__ inline size_t fp4_scale_offset(int64_t row, int64_t block, int64_t tiles) {
+  return static_cast<size_t>((row >> 7) * tiles + (block >> 2)) * 512 + static_cast<size_t>((row & 31) * 16) +
+         static_cast<size_t>(((row >> 5) & 3) * 4) + static_cast<size_t>(block & 3);
+}
+
+// A quotient x / (s rs) of a bf16 x by an e4m3 scale and a power of two lies on
+// a rounding border of e2m1 (0.25 .. 5) or at least 2^-10 away from every border,
+// while its fp32 approximation x * (1 / (s rs)) is off by at most 2^-20. Rounding
+// the product to a multiple of 2^-12 (adding and taking off 1.5 * 2^11, in the
+// fused multiply-add) therefore puts the border cases exactly on the border and
+// moves no other one across, without a division per value.
+__device__ __forceinline__ float e2m1_grid(float x, float inv) {
+  const float c = 0x1.8p11f;
+  return __fadd_rn(__fmaf_rn(x, inv, c), -c);
+}
+
+// Eight values to eight e2m1 codes, value i in bits 4i .. 4i+3.
+__device__ __forceinline__ uint32_t e2m1x8(const float *v) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// The two bf16 of a word as fp32.
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Maximum of the magnitudes of packed bf16 pairs, by their bits (a NaN is above
+// infinity, so it is kept): running value in packed form.
+__device__ __forceinline__ uint32_t amax_bf16x2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+__device__ __forceinline__ uint32_t amax_fold(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+constexpr uint32_t kBf16Inf = 0x7f80u;  // magnitudes from here up are infinite or NaN
+
+// NVFP4 row scale from the bits of the row's largest magnitude.
+__device__ __forceinline__ float nvfp4_row_scale(uint32_t amax) {
+  if (amax == 0) return 1.f;
+  if (amax >= kBf16Inf) return __uint_as_float(0x7fc00000u);
+  const int e = min(max(static_cast<int>(amax >> 7) - 127 - 10, -110), 117);
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// NVFP4 block: e4m3 scale byte and the factor that takes x to its code's grid
+// (0 for a block whose scale is 0). rs_inv = 1 / row scale (0 for a row that is
+// not finite: every scale and code is 0 and the NaN row scale speaks for it).
+__device__ __forceinline__ uint32_t nvfp4_block_scale(uint32_t amax, float rs_inv, float *inv) {
+  const float t = rs_inv != 0.f ? __fdiv_rn(__uint_as_float(amax << 16) * rs_inv, 6.f) : 0.f;
+  const __nv_fp8_storage_t b = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
+  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
+  *inv = s > 0.f ? __frcp_rn(s) * rs_inv : 0.f;
+  return b;
+}
+
+// MXFP4 block: e8m0 scale byte and 1 / scale (exact; 0 for a block that is not finite).
+__device__ __forceinline__ uint32_t mxfp4_block_scale(uint32_t amax, float *inv) {
+  if (amax >= kBf16Inf) {
+    *inv = 0.f;
+    return 255u;
+  }
+  const int b = max(static_cast<int>(amax >> 7) - 2, 0);
+  *inv = __uint_as_float(static_cast<uint32_t>(254 - b) << 23);
+  return static_cast<uint32_t>(b);
+}
+
+// Scale bytes to fp32.
+__device__ __forceinline__ float e4m3_to_f32(uint32_t b) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3)));
+}
+__device__ __forceinline__ float e8m0_to_f32(uint32_t b) {
+  return __uint_as_float(b == 255u ? 0x7fc00000u : b == 0u ? 0x00400000u : b << 23);
+}
+
+}  // namespace cm

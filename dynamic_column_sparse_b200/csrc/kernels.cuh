@@ -126,6 +126,77 @@ int64_t mass_row_floats(int64_t T);
 cudaError_t launch_attn_mass_select(const MassParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                                     cudaStream_t s);
 
+// ------------------------------------------------------------------ 4-bit microscaled rows (fp4.cuh)
+
+struct Fp4QuantParams {
+  int64_t rows, cols;
+  int fmt;                // Fp4Format
+  const uint16_t *x;      // [rows][cols] bf16 (quantiser)
+  uint8_t *codes;         // [rows][cols / 2]
+  uint8_t *scales;        // fp4_scale_bytes(rows, cols, fmt)
+  float *row_scales;      // [rows] (NVFP4)
+  int *status;
+};
+cudaError_t launch_quantize_fp4_rows(const Fp4QuantParams &p, cudaStream_t s);
+// out [rows][cols], fp32 or bf16.
+cudaError_t launch_dequantize_fp4_rows(const Fp4QuantParams &p, bool f32, void *out, cudaStream_t s);
+
+// out[t][n] = act(ra[t] rb[n] sum_k x[t][k] w[n][k] + bias[n]), x and w 4-bit
+// microscaled rows. tm_x / tm_w: byte maps over the codes (128-byte boxes), tm_out:
+// a map over out (boxes of 32 rows x 128 bytes).
+struct LinearFp4Params {
+  int T, N, K, fmt;
+  int gelu, out_f32;
+  const uint8_t *sx, *sw;      // block scales
+  const float *rx, *rw;        // row scales (NVFP4)
+  const uint16_t *bias;        // [N] bf16 or nullptr
+  int *status;
+};
+constexpr int kLinearTileM = 128, kLinearTileN = 128;
+cudaError_t launch_linear_fp4(const LinearFp4Params &p, const CUtensorMap &tm_x, const CUtensorMap &tm_w,
+                              const CUtensorMap &tm_out, cudaStream_t s);
+
+// ------------------------------------------------------------------ norms with gate and residual
+
+enum NormKind : int { kNormNone = 0, kNormLayer = 1, kNormRms = 2 };
+enum NormOut : int { kOutBf16 = 0, kOutE4m3 = 1, kOutNvfp4 = 2, kOutMxfp4 = 3 };
+
+struct NormParams {
+  int64_t T;
+  int D, B;
+  int res_f32, y_f32, mod_f32;  // fp32 instead of bf16
+  int norm, post_norm, out_format;
+  float eps, res_scale;
+  const void *res, *y;          // [T][D]; y may be nullptr
+  const void *post_weight;      // [D] bf16 or nullptr
+  const void *gate;             // [B][ld_mod] or nullptr
+  void *res_out;                // [T][D] or nullptr
+  const void *weight, *bias;    // [D] bf16 or nullptr
+  const void *scale, *shift;    // [B][ld_mod] or nullptr
+  int64_t ld_mod;
+  const int32_t *offsets;       // [B + 1] or nullptr (one sample of all rows)
+  void *out;                    // [T][D] bf16, e4m3 codes [T][D], 4-bit codes [T][D / 2], or nullptr
+  uint8_t *out_scales;
+  float *out_row_scales;
+  int *status;
+};
+cudaError_t launch_norm_residual(const NormParams &p, cudaStream_t s);
+
+// ------------------------------------------------------------------ heads out of a fused projection
+
+struct HeadsParams {
+  int64_t T;
+  int h, halves;
+  int64_t ld;                   // row stride of qkv in elements
+  float eps;
+  const uint16_t *qkv;          // [T][ld], q, k, v heads in columns 0 .. 3 h 128
+  const uint16_t *q_weight, *k_weight;  // [128]
+  const float *cos, *sin;       // [T][64]
+  uint16_t *q, *k, *v;          // [T][h][128]
+  int *status;
+};
+cudaError_t launch_qk_norm_rope(const HeadsParams &p, cudaStream_t s);
+
 // One CTA waiting on a barrier nothing signals (bounded: records a timeout).
 cudaError_t launch_selftest_wait(int *status, cudaStream_t s);
 

@@ -1,0 +1,355 @@
+// norm.cu - the norms around a block's layers fused with its gate and residual.
+//
+// For every row t of sample b:
+//   r = res_scale * res + gate[b] * post(y)          post: none, RMS or layer norm (* post_weight)
+//   h = pre(r) * weight + bias, * (1 + scale[b]) + shift[b]
+// r goes out in the residual stream's type, h as bf16 or as quantised rows
+// (e4m3 with a row scale, or 4-bit microscaled: fp4.cuh) for the next
+// projection; quantised rows are those of the bf16-rounded h, so they equal
+// what the stand-alone quantisers give for the bf16 output. h is computed from
+// the unrounded fp32 r.
+//
+// HBM bound: each row is read once, kept in registers as fp32 and written once;
+// the statistics are two-pass in registers (a mean, then squares about it), the
+// partial sums of a row's warps joined through shared memory by the pairwise
+// rule for means and squares, so no large mean cancels.
+//
+// A row is held by one warp (up to 1024 columns) or by 4, 8 or 16 warps of one
+// CTA, NV groups of 8 columns per thread; column group v * G + t belongs to
+// thread t, so every access is 16 bytes per lane and consecutive over a warp.
+#include <algorithm>
+
+#include "fp4.cuh"
+#include "kernels.cuh"
+
+namespace cm {
+namespace {
+
+__device__ __forceinline__ void load8(const void *p, int f32, int64_t i, float *v) {
+  if (f32) {
+    const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    const float4 a = s[0], b = s[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(w[e]), v[2 * e + 1] = bf16_hi(w[e]);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float *v) {
+  return make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Statistics of one row over its W warps. `slot` alternates between two shared
+// buffers, so one barrier per statistic is enough.
+template <int W>
+struct RowStats {
+  float2 (*buf)[16];  // [2][16]
+  int slot = 0;
+
+  // mean and 1 / sqrt(variance + eps) of the row (RMS: mean 0, mean square)
+  template <int NV>
+  __device__ __forceinline__ float2 norm(const float (&r)[NV][8], const int nv, int warp, int lane, int G, int D,
+                                         bool layer, float eps) {
+    // columns held by this warp
+    float s = 0.f, q = 0.f;
+    int n8 = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (v < nv) {
+        ++n8;
+        if (layer) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s += r[v][e];
+        }
+      }
+    float mean = 0.f, n = 0.f;
+    if (layer) {
+      s = warp_sum(s);
+      n = 8.f * warp_sum(static_cast<float>(n8));
+      mean = n > 0.f ? s / n : 0.f;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (v < nv) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = r[v][e] - mean;
+          q = fmaf(d, d, q);
+        }
+      }
+    q = warp_sum(q);
+    if (W > 1) {
+      // join the warps: squares about the row's mean = squares about each
+      // warp's mean + n_w (mean_w - mean)^2
+      if (lane == 0) buf[slot][warp] = make_float2(s, q);
+      __syncthreads();
+      float S = 0.f, Q = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) S += buf[slot][w].x;
+      const float m = S / static_cast<float>(D);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        Q += buf[slot][w].y;
+        if (layer) {
+          // columns of warp w: 8 per lane and full group, fewer in the last
+          int nw = 0;
+#pragma unroll
+          for (int v = 0; v < NV; ++v) nw += min(max(D / 8 - v * G - w * 32, 0), 32);
+          const float nf = 8.f * static_cast<float>(nw);
+          const float d = nw > 0 ? buf[slot][w].x / nf - m : 0.f;
+          Q = fmaf(nf * d, d, Q);
+        }
+      }
+      slot ^= 1;
+      mean = layer ? m : 0.f;
+      q = Q;
+    }
+    return make_float2(mean, 1.f / sqrtf(q / static_cast<float>(D) + eps));
+  }
+
+  // largest bf16 magnitude of the row, as bits
+  __device__ __forceinline__ uint32_t amax(uint32_t m, int warp, int lane) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (W > 1) {
+      if (lane == 0) buf[slot][warp].x = __uint_as_float(m);
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < W; ++w) m = max(m, __float_as_uint(buf[slot][w].x));
+      slot ^= 1;
+    }
+    return m;
+  }
+};
+
+// The sample of row t: the last b with offsets[b] <= t, -1 for a row of no sample.
+__device__ __forceinline__ int sample_of(const int32_t *off, int B, int64_t t) {
+  if (t < off[0] || t >= off[B]) return -1;
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+template <int W, int NV>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(const NormParams p) {
+  constexpr int G = 32 * W;                   // threads per row
+  constexpr int kRows = (W == 1 ? 128 : G) / G;  // rows a CTA works on at a time
+  __shared__ float2 buf[2][16];
+  if (*(volatile const int *)p.status != kDevOk) return;
+  const int t = threadIdx.x % G, warp = t >> 5, lane = t & 31;
+  const int D = p.D, ng = D / 8;
+  const int nv = t < ng ? (ng - 1 - t) / G + 1 : 0;  // column groups of this thread
+  RowStats<W> st{buf};
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G; row < p.T;
+       row += static_cast<int64_t>(gridDim.x) * kRows) {
+    int b = 0;
+    if (p.offsets != nullptr) {
+      b = sample_of(p.offsets, static_cast<int>(p.B), row);
+      if (b < 0) continue;  // the same for all threads of the row
+    }
+    const int64_t mod = static_cast<int64_t>(b) * p.ld_mod;
+    const int64_t base = row * D;
+    float r[NV][8];
+    if (p.y != nullptr) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (v < nv) load8(p.y, p.y_f32, base + (v * G + t) * 8, r[v]);
+      float2 ms = make_float2(0.f, 1.f);
+      if (p.post_norm != kNormNone)
+        ms = st.template norm<NV>(r, nv, warp, lane, G, D, p.post_norm == kNormLayer, p.eps);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (v < nv) {
+          const int c = (v * G + t) * 8;
+          float a[8];
+          if (p.post_norm != kNormNone) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[v][e] = (r[v][e] - ms.x) * ms.y;
+            if (p.post_weight != nullptr) {
+              load8(p.post_weight, 0, c, a);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) r[v][e] *= a[e];
+            }
+          }
+          if (p.gate != nullptr) {
+            load8(p.gate, p.mod_f32, mod + c, a);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[v][e] *= a[e];
+          }
+          load8(p.res, p.res_f32, base + c, a);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[v][e] = fmaf(p.res_scale, a[e], r[v][e]);
+        }
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (v < nv) {
+          load8(p.res, p.res_f32, base + (v * G + t) * 8, r[v]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[v][e] *= p.res_scale;
+        }
+    }
+    if (p.res_out != nullptr) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (v < nv) {
+          const int64_t i = base + (v * G + t) * 8;
+          if (p.res_f32) {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.res_out) + i);
+            o[0] = make_float4(r[v][0], r[v][1], r[v][2], r[v][3]);
+            o[1] = make_float4(r[v][4], r[v][5], r[v][6], r[v][7]);
+          } else {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.res_out) + i) = pack8(r[v]);
+          }
+        }
+    }
+    if (p.out == nullptr) continue;
+    const float2 ms = st.template norm<NV>(r, nv, warp, lane, G, D, p.norm == kNormLayer, p.eps);
+    uint4 h[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      h[v] = make_uint4(0, 0, 0, 0);
+      if (v < nv) {
+        const int c = (v * G + t) * 8;
+        float a[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[v][e] = (r[v][e] - ms.x) * ms.y;
+        if (p.weight != nullptr) {
+          load8(p.weight, 0, c, a);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[v][e] *= a[e];
+        }
+        if (p.bias != nullptr) {
+          load8(p.bias, 0, c, a);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[v][e] += a[e];
+        }
+        if (p.scale != nullptr) {
+          load8(p.scale, p.mod_f32, mod + c, a);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[v][e] = fmaf(r[v][e], a[e], r[v][e]);
+        }
+        if (p.shift != nullptr) {
+          load8(p.shift, p.mod_f32, mod + c, a);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[v][e] += a[e];
+        }
+        h[v] = pack8(r[v]);
+      }
+    }
+    if (p.out_format == kOutBf16) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (v < nv)
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + base + (v * G + t) * 8) = h[v];
+      continue;
+    }
+    // quantised rows of the bf16 values in h
+    uint32_t m[NV];
+    uint32_t row_max = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      m[v] = amax_fold(amax_bf16x2(amax_bf16x2(amax_bf16x2(amax_bf16x2(0, h[v].x), h[v].y), h[v].z), h[v].w));
+      row_max = max(row_max, m[v]);
+    }
+    if (p.out_format != kOutMxfp4) row_max = st.amax(row_max, warp, lane);
+    if (p.out_format == kOutE4m3) {
+      const float amax = __uint_as_float(row_max << 16);
+      const float inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 1.f;
+      if (t == 0) p.out_row_scales[row] = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (v < nv) {
+          const uint32_t w[4] = {h[v].x, h[v].y, h[v].z, h[v].w};
+          uint32_t o[2] = {0, 0};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t c0 = __nv_cvt_float_to_fp8(__fmul_rn(bf16_lo(w[e]), inv), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t c1 = __nv_cvt_float_to_fp8(__fmul_rn(bf16_hi(w[e]), inv), __NV_SATFINITE, __NV_E4M3);
+            o[e >> 1] |= (c0 | c1 << 8) << (16 * (e & 1));
+          }
+          *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + base + (v * G + t) * 8) = make_uint2(o[0], o[1]);
+        }
+      continue;
+    }
+    const bool nv4 = p.out_format == kOutNvfp4;
+    float rs_inv = 1.f;
+    if (nv4) {
+      const float rs = nvfp4_row_scale(row_max);
+      rs_inv = row_max >= kBf16Inf ? 0.f : __frcp_rn(rs);
+      if (t == 0) p.out_row_scales[row] = rs;
+    }
+    const int64_t tiles = fp4_scale_tiles(D, nv4 ? kNvfp4 : kMxfp4);
+    const int pad_ng = (D + 255) / 256 * 32;  // column groups that carry scale bytes
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int g = v * G + t;
+      // blocks of 16 or 32 columns: 2 or 4 neighbouring lanes
+      uint32_t am = max(m[v], __shfl_xor_sync(0xffffffffu, m[v], 1));
+      float inv;
+      uint32_t sb;
+      if (nv4) {
+        sb = nvfp4_block_scale(am, rs_inv, &inv);
+      } else {
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        sb = mxfp4_block_scale(am, &inv);
+      }
+      if (g >= ng) sb = 0;
+      const int kl = nv4 ? 2 : 4;  // lanes per block
+      uint32_t word = sb;
+#pragma unroll
+      for (int i = 1; i < 4; ++i) word |= __shfl_down_sync(0xffffffffu, sb, i * kl) << (8 * i);
+      if ((lane & (4 * kl - 1)) == 0 && g < pad_ng)
+        *reinterpret_cast<uint32_t *>(p.out_scales + fp4_scale_offset(row, g / kl, tiles)) = word;
+      if (g < ng) {
+        const uint32_t w[4] = {h[v].x, h[v].y, h[v].z, h[v].w};
+        float q[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          q[2 * e] = nv4 ? e2m1_grid(bf16_lo(w[e]), inv) : bf16_lo(w[e]) * inv;
+          q[2 * e + 1] = nv4 ? e2m1_grid(bf16_hi(w[e]), inv) : bf16_hi(w[e]) * inv;
+        }
+        static_cast<uint32_t *>(p.out)[row * (D / 8) + g] = e2m1x8(q);
+      }
+    }
+  }
+}
+
+template <int W>
+cudaError_t launch_w(const NormParams &p, cudaStream_t s) {
+  const int need = (p.D / 8 + 32 * W - 1) / (32 * W);
+  const int rows = W == 1 ? 4 : 1;
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((p.T + rows - 1) / rows, 148 * 16));
+  const unsigned threads = W == 1 ? 128 : 32 * W;
+  switch (need) {
+    case 1: norm_residual_kernel<W, 1><<<blocks, threads, 0, s>>>(p); break;
+    case 2: norm_residual_kernel<W, 2><<<blocks, threads, 0, s>>>(p); break;
+    case 3: norm_residual_kernel<W, 3><<<blocks, threads, 0, s>>>(p); break;
+    default: norm_residual_kernel<W, 4><<<blocks, threads, 0, s>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_norm_residual(const NormParams &p, cudaStream_t s) {
+  if (p.T <= 0) return cudaSuccess;
+  if (p.D <= 32 * 8 * 4) return launch_w<1>(p, s);
+  if (p.D <= 128 * 8 * 4) return launch_w<4>(p, s);
+  if (p.D <= 256 * 8 * 4) return launch_w<8>(p, s);
+  return launch_w<16>(p, s);
+}
+
+}  // namespace cm

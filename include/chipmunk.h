@@ -180,6 +180,7 @@ typedef struct chipmunk_refresh_args {
 #define CHIPMUNK_OP_ATTN_DELTA   2
 #define CHIPMUNK_OP_REFRESH      3
 #define CHIPMUNK_OP_MLP_DELTA_FP8 4
+#define CHIPMUNK_OP_LINEAR_FP4   5
 
 /*
  * Top-k column selection (post: Chipmunk "dynamically chooses which ones to
@@ -353,6 +354,175 @@ CHIPMUNK_API chipmunk_status chipmunk_gather_cols(const void *a_cache, int64_t n
                                      const int32_t *idx, int32_t k, void *packed, chipmunk_stream stream);
 CHIPMUNK_API chipmunk_status chipmunk_scatter_cols(const void *packed, int64_t nb, int64_t H, int32_t Bt,
                                       const int32_t *idx, int32_t k, void *a_cache, chipmunk_stream stream);
+
+/*
+ * What stands around a block's two sparse layers
+ * ----------------------------------------------
+ * A diffusion-transformer block wraps its attention and its MLP in modulated
+ * norms, gates and residuals, dense projections, and a head split with the norm
+ * and rotation of q and k. The calls below cover those, so that a block runs on
+ * this library alone. (The post names the sparse layers only; these operators are
+ * written from their usual definitions.)
+ */
+#define CHIPMUNK_BF16 0
+#define CHIPMUNK_FP32 1
+
+/*
+ * 4-bit microscaled rows: value = code * block scale (* row scale), codes e2m1
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives).
+ *   format      CHIPMUNK_NVFP4: blocks of 16 columns, e4m3 block scales and one
+ *               fp32 row scale, a power of two:
+ *                 row_scale = 2^clamp(floor(log2 max|row|) - 10, -110, 117)
+ *                             (1 for an all-zero row, NaN for one with an infinity or NaN)
+ *                 block scale = e4m3(max|block| / (6 row_scale))
+ *                 code = e2m1(x / (block scale * row_scale)), 0 where that scale is 0
+ *               CHIPMUNK_MXFP4: blocks of 32 columns, e8m0 block scales (a byte b
+ *               is 2^(b-127), 255 is NaN), no row scale:
+ *                 block scale = 2^max(floor(log2 max|block|) - 2, -127)
+ *                               (NaN for a block with an infinity or NaN)
+ *                 code = e2m1(x / block scale)
+ *               Roundings are to nearest, ties to even, saturating at +-6.
+ *   rows, cols  cols a multiple of 32, 32..65536; rows >= 0
+ *   codes       [rows][cols / 2] bytes, the lower column in the low nibble
+ *   scales      chipmunk_fp4_scale_bytes(rows, cols, format) bytes, in the order of
+ *               the tensor core's scale operand: tiles of 128 rows x 4 blocks, 512
+ *               bytes each, byte (r % 32) * 16 + (r % 128) / 32 * 4 + block % 4; the
+ *               tiles of 128 rows consecutive along the columns, padded to whole
+ *               256 columns (padding blocks of a row hold 0; bytes of rows past
+ *               the last are not written)
+ *   row_scales  [rows] fp32 (NVFP4; not used and may be NULL for MXFP4)
+ */
+#define CHIPMUNK_NVFP4 0
+#define CHIPMUNK_MXFP4 1
+typedef struct chipmunk_fp4_rows {
+  int64_t rows, cols;
+  int32_t format;
+  void *codes, *scales;
+  float *row_scales;
+} chipmunk_fp4_rows;
+
+/* Bytes of the block scales of rows x cols (0 for sizes outside the supported set). */
+CHIPMUNK_API size_t chipmunk_fp4_scale_bytes(int64_t rows, int64_t cols, int32_t format);
+
+/* Quantises x [rows][cols] bf16 into q. */
+CHIPMUNK_API chipmunk_status chipmunk_quantize_fp4_rows(const void *x, const chipmunk_fp4_rows *q,
+                                                        chipmunk_stream stream);
+
+/*
+ * The values q stands for, out [rows][cols] of out_type (CHIPMUNK_BF16 or
+ * CHIPMUNK_FP32). They are exact in bf16, save that a value above the largest
+ * finite one becomes an infinity.
+ */
+CHIPMUNK_API chipmunk_status chipmunk_dequantize_fp4_rows(const chipmunk_fp4_rows *q, int32_t out_type, void *out,
+                                                          chipmunk_stream stream);
+
+/*
+ * Dense projection on 4-bit operands (tcgen05 block-scaled MMAs, fp32 sums):
+ *   out[t][n] = act(sum_k X[t][k] W[n][k] + bias[n])
+ * X, W being the values of 4-bit rows of one format.
+ *   T >= 1, N a multiple of 8 in 8..2^20, K = w.cols
+ *   x         [T][K] bf16, quantised by the call into the workspace; or NULL, and
+ *   xq        T quantised rows of K columns (ignored when x is given)
+ *   w         N quantised rows of K columns
+ *   bias      [N] bf16 or NULL
+ *   act       CHIPMUNK_ACT_NONE or CHIPMUNK_ACT_GELU (tanh form)
+ *   out       [T][N] of out_type
+ * Workspace: chipmunk_workspace_bytes(CHIPMUNK_OP_LINEAR_FP4, a) bytes (the
+ * quantised x; none when x is NULL), 16-byte aligned.
+ */
+#define CHIPMUNK_ACT_NONE 0
+#define CHIPMUNK_ACT_GELU 1
+typedef struct chipmunk_linear_fp4_args {
+  int64_t T, N;
+  int32_t act, out_type;
+  const void *x;
+  chipmunk_fp4_rows xq, w;
+  const void *bias;
+  void *out;
+} chipmunk_linear_fp4_args;
+
+CHIPMUNK_API chipmunk_status chipmunk_linear_fp4(const chipmunk_linear_fp4_args *a, void *ws, size_t ws_bytes,
+                                                 chipmunk_stream stream);
+
+/*
+ * Norms around a layer, with its gate and the residual. For row t of sample b:
+ *   r = res_scale * res[t] + gate[b] * post(y[t])
+ *   h = (pre(r) * weight + bias) * (1 + scale[b]) + shift[b]
+ * res_out[t] = r in the residual's type, out[t] = h. Sums and statistics are
+ * fp32; h is taken from the unrounded r.
+ *   T >= 1, D a multiple of 8 in 8..16384, B >= 1 samples
+ *   res         [T][D] of res_type
+ *   y           [T][D] of y_type, or NULL (then gate and post_weight are NULL,
+ *               post_norm is CHIPMUNK_NORM_NONE)
+ *   post_norm   CHIPMUNK_NORM_NONE, _LAYER or _RMS of y over D; post_weight [D]
+ *               bf16 or NULL
+ *   gate, scale, shift  of mod_type, or NULL (gate 1, scale 0, shift 0): row b at
+ *               b * ld_mod elements (a multiple of 8, >= D), so that the three may
+ *               be column ranges of one modulation projection
+ *   res_out     [T][D] of res_type, or NULL; may be res itself
+ *   norm        CHIPMUNK_NORM_LAYER or _RMS of r over D (not looked at when out is
+ *               NULL); weight, bias [D] bf16 or NULL
+ *   eps         added to the variance or mean square (both norms), >= 0
+ *   offsets     [B + 1] int32, ascending: sample b holds rows offsets[b] ..
+ *               offsets[b + 1] - 1 (none when equal). Rows below offsets[0] or from
+ *               offsets[B] on belong to no sample and are left as they were. NULL:
+ *               all rows are sample 0 and B must be 1.
+ *   out         [T][D] bf16, or quantised rows of the bf16-rounded h, the same as
+ *               the stand-alone quantisers give for them; NULL: only res_out.
+ *   out_format  CHIPMUNK_OUT_BF16; CHIPMUNK_OUT_E4M3: codes [T][D] in out, row
+ *               scales [T] in out_row_scales (D a multiple of 16; values must be
+ *               finite); CHIPMUNK_OUT_NVFP4 / _MXFP4: codes [T][D / 2] in out, block scales of T
+ *               rows in out_scales, row scales (NVFP4) in out_row_scales (D a
+ *               multiple of 32)
+ * Apart from res_out = res, outputs must not overlap inputs. Needs no workspace.
+ */
+#define CHIPMUNK_NORM_NONE  0
+#define CHIPMUNK_NORM_LAYER 1
+#define CHIPMUNK_NORM_RMS   2
+#define CHIPMUNK_OUT_BF16   0
+#define CHIPMUNK_OUT_E4M3   1
+#define CHIPMUNK_OUT_NVFP4  2
+#define CHIPMUNK_OUT_MXFP4  3
+typedef struct chipmunk_norm_args {
+  int64_t T, D, B;
+  int32_t res_type, y_type, mod_type;
+  int32_t post_norm, norm, out_format;
+  float eps, res_scale;
+  const void *res, *y, *post_weight, *gate;
+  void *res_out;
+  const void *weight, *bias, *scale, *shift;
+  int64_t ld_mod;
+  const int32_t *offsets;
+  void *out, *out_scales;
+  float *out_row_scales;
+} chipmunk_norm_args;
+
+CHIPMUNK_API chipmunk_status chipmunk_norm_residual(const chipmunk_norm_args *a, chipmunk_stream stream);
+
+/*
+ * Heads out of a fused projection: columns 0..h*128-1 of a row of qkv are its q
+ * heads, the next h*128 its k heads, the next h*128 its v heads (columns beyond
+ * are not read). For each q and k head x:
+ *   x <- x / sqrt(mean(x^2) + eps) * weight, then rotated by its token's angles:
+ *   (a, b) <- (a cos - b sin, a sin + b cos) for the 64 pairs (a, b) = columns
+ *   (2i, 2i+1) (CHIPMUNK_PAIRS_INTERLEAVED) or (i, i+64) (CHIPMUNK_PAIRS_HALVES)
+ * v heads are copied. Results are the contiguous tensors of chipmunk_attn_args.
+ *   T >= 1, h in 1..1024, T * h < 2^31, ld >= 3*h*128 a multiple of 8
+ *   qkv [T][ld] bf16; q_weight, k_weight [128] bf16; cos, sin [T][64] fp32
+ *   q, k, v [T][h][128] bf16; eps >= 0. Outputs must not overlap inputs.
+ */
+#define CHIPMUNK_PAIRS_INTERLEAVED 0
+#define CHIPMUNK_PAIRS_HALVES      1
+typedef struct chipmunk_heads_args {
+  int64_t T, ld;
+  int32_t h, pairs;
+  float eps;
+  const void *qkv, *q_weight, *k_weight;
+  const float *cos, *sin;
+  void *q, *k, *v;
+} chipmunk_heads_args;
+
+CHIPMUNK_API chipmunk_status chipmunk_qk_norm_rope(const chipmunk_heads_args *a, chipmunk_stream stream);
 
 /*
  * Workspace bytes an operation needs for the given arguments (a pointer to
