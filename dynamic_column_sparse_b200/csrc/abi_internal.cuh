@@ -18,10 +18,10 @@ chipmunk_status record_errorf(chipmunk_status st, const char *fmt, ...) __attrib
 // Checks that the current device is sm_100 and resolves its status word.
 chipmunk_status device_ready(int **status_out);
 
-// Rank-2 tensor map with 128-byte swizzle over rows x cols elements, row-major with
+// Rank-2 tensor map (128-byte swizzle or none) over rows x cols elements, row-major with
 // `pitch` bytes between rows; box = box_cols x box_rows.
 chipmunk_status encode_map2d(CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t rows, uint64_t cols,
-                             uint64_t pitch, uint32_t box_cols, uint32_t box_rows, const char *what);
+                             uint64_t pitch, uint32_t box_cols, uint32_t box_rows, bool swizzled, const char *what);
 
 // chipmunk_mlp_delta with its delta scratch taken from get_scratch instead of
 // a caller workspace. The arguments are checked first; a step that needs more

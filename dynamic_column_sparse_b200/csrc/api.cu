@@ -297,12 +297,12 @@ chipmunk_status record_errorf(chipmunk_status st, const char *fmt, ...) {
 chipmunk_status device_ready(int **status_out) { return device_setup(status_out); }
 
 chipmunk_status encode_map2d(CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t rows, uint64_t cols,
-                             uint64_t pitch, uint32_t box_cols, uint32_t box_rows, const char *what) {
+                             uint64_t pitch, uint32_t box_cols, uint32_t box_rows, bool swizzled, const char *what) {
   const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
   const cuuint32_t box[2] = {box_cols, box_rows}, es[2] = {1, 1};
   CUresult r = g_encode(m, type, 2, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(CHIPMUNK_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, int(r));
   return CHIPMUNK_OK;
 }

@@ -168,13 +168,18 @@ chipmunk_status chipmunk_linear_fp4(const chipmunk_linear_fp4_args *a, void *ws,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const uint64_t row_bytes = uint64_t(a->w.cols) / 2;
   const bool f32 = a->out_type == CHIPMUNK_FP32;
-  CUtensorMap tm_x, tm_w, tm_out;
-  CM_CHECK(cm::encode_map2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq.codes, a->T, row_bytes, row_bytes, 128,
-                            cm::kLinearTileM, "x codes"));
-  CM_CHECK(cm::encode_map2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->w.codes, a->N, row_bytes, row_bytes, 128,
-                            cm::kLinearTileN, "w codes"));
-  CM_CHECK(cm::encode_map2d(&tm_out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->out,
-                            a->T, a->N, uint64_t(a->N) * (f32 ? 4 : 2), f32 ? 32 : 64, 32, "out"));
+  cm::LinearFp4Maps m;
+  const CUtensorMapDataType bytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  CM_CHECK(cm::encode_map2d(&m.x, bytes, xq.codes, a->T, row_bytes, row_bytes, 128, 128, true, "x codes"));
+  CM_CHECK(cm::encode_map2d(&m.w, bytes, a->w.codes, a->N, row_bytes, row_bytes, 128, 128, true, "w codes"));
+  const uint64_t tiles = cm::fp4_scale_tiles(a->w.cols, a->w.format);
+  const uint32_t per_stage = a->w.format == CHIPMUNK_NVFP4 ? 4 : 2;
+  CM_CHECK(cm::encode_map2d(&m.sx, CU_TENSOR_MAP_DATA_TYPE_INT32, xq.scales, (a->T + 127) / 128 * tiles, 128, 512, 128,
+                            per_stage, false, "x scales"));
+  CM_CHECK(cm::encode_map2d(&m.sw, CU_TENSOR_MAP_DATA_TYPE_INT32, a->w.scales, (a->N + 127) / 128 * tiles, 128, 512,
+                            128, per_stage, false, "w scales"));
+  CM_CHECK(cm::encode_map2d(&m.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->out,
+                            a->T, a->N, uint64_t(a->N) * (f32 ? 4 : 2), f32 ? 32 : 64, 32, true, "out"));
   if (a->x != nullptr)
     CM_CUDA(cm::launch_quantize_fp4_rows(quant_params(a->x, &xq, status), s), "4-bit quantise launch");
   cm::LinearFp4Params p{int(a->T),
@@ -183,13 +188,11 @@ chipmunk_status chipmunk_linear_fp4(const chipmunk_linear_fp4_args *a, void *ws,
                         a->w.format == CHIPMUNK_NVFP4 ? cm::kNvfp4 : cm::kMxfp4,
                         a->act == CHIPMUNK_ACT_GELU,
                         f32,
-                        static_cast<const uint8_t *>(xq.scales),
-                        static_cast<const uint8_t *>(a->w.scales),
                         xq.row_scales,
                         a->w.row_scales,
                         static_cast<const uint16_t *>(a->bias),
                         status};
-  CM_CUDA(cm::launch_linear_fp4(p, tm_x, tm_w, tm_out, s), "4-bit linear launch");
+  CM_CUDA(cm::launch_linear_fp4(p, m, s), "4-bit linear launch");
   return CHIPMUNK_OK;
 }
 

@@ -141,20 +141,22 @@ cudaError_t launch_quantize_fp4_rows(const Fp4QuantParams &p, cudaStream_t s);
 // out [rows][cols], fp32 or bf16.
 cudaError_t launch_dequantize_fp4_rows(const Fp4QuantParams &p, bool f32, void *out, cudaStream_t s);
 
-// out[t][n] = act(ra[t] rb[n] sum_k x[t][k] w[n][k] + bias[n]), x and w 4-bit
-// microscaled rows. tm_x / tm_w: byte maps over the codes (128-byte boxes), tm_out:
-// a map over out (boxes of 32 rows x 128 bytes).
+// out[t][n] = act(rx[t] rw[n] sum_k x[t][k] w[n][k] + bias[n]), x and w 4-bit
+// microscaled rows.
 struct LinearFp4Params {
   int T, N, K, fmt;
   int gelu, out_f32;
-  const uint8_t *sx, *sw;      // block scales
   const float *rx, *rw;        // row scales (NVFP4)
   const uint16_t *bias;        // [N] bf16 or nullptr
   int *status;
 };
-constexpr int kLinearTileM = 128, kLinearTileN = 128;
-cudaError_t launch_linear_fp4(const LinearFp4Params &p, const CUtensorMap &tm_x, const CUtensorMap &tm_w,
-                              const CUtensorMap &tm_out, cudaStream_t s);
+// Byte maps over the codes (boxes of 128 bytes x 128 rows), maps over the block
+// scales as rows of 128 words, one 512-byte scale tile each (boxes of one stage's tiles of
+// 128 rows), and a map over out (boxes of 128 bytes x 32 rows).
+struct LinearFp4Maps {
+  CUtensorMap x, w, sx, sw, out;
+};
+cudaError_t launch_linear_fp4(const LinearFp4Params &p, const LinearFp4Maps &m, cudaStream_t s);
 
 // ------------------------------------------------------------------ norms with gate and residual
 

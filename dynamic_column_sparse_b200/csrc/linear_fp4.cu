@@ -3,14 +3,22 @@
 //   out[t][n] = act(rx[t] rw[n] sum_k x[t][k] w[n][k] + bias[n])
 // with x [T][K] and w [N][K] as codes, block scales and (NVFP4) row scales.
 //
-// Persistent, one CTA per SM, one 128 x 128 output tile at a time, tiles walked
-// weight-slice fastest so a row block of x is read from HBM once while the
-// weights stay in L2. Warp 0 fills a ring of stages of 256 columns: both code tiles
-// by TMA (128-byte swizzle), both tiles' block scales by bulk copies of their
-// consecutive 512-byte scale tiles. Warp 1 copies a stage's scales to TMEM and
-// issues its four MMAs. Warps 2-5 drain one accumulator (scales, bias,
-// activation, rounding, TMA stores through swizzled shared memory) while the
-// other is being filled.
+// Persistent, one CTA per SM. Two forms: a CTA pair (cta_group::2) on a 256 x
+// 256 output tile, each CTA holding 128 rows of x, 128 rows of w and 128 rows of
+// the result; and one CTA on a 128 x 128 tile where the larger tiles would leave SMs
+// idle. Tiles are walked weight-slice fastest, so a row block of x is read
+// from HBM once while the weights stay in L2.
+//
+// Warp 0 fills a ring of stages of 256 columns with TMA: code tiles
+// (128-byte swizzle) and the block scales' 512-byte tiles. Warp 1 (of the leading CTA)
+// copies scales to TMEM and issues the MMAs. The scale columns are a ring of
+// their own, one slot per scale tile, filled one slot ahead of the MMAs: with a
+// copy and its MMAs back to back the tensor core idled more than half the time
+// (546 of 1240 cycles per stage busy, ncu). Warps 2-5 drain one accumulator (scales,
+// bias, activation, rounding, TMA stores through swizzled shared memory) while
+// the other is being filled. At 256 columns the two accumulators share 64 TMEM
+// columns, which leaves 64 for the scales: the shared columns are drained first and the next
+// tile's MMAs wait for them only.
 #include <algorithm>
 
 #include "fp4.cuh"
@@ -20,54 +28,76 @@
 namespace cm {
 namespace {
 
+// CG CTAs per tile; BN tile columns; 128 * CG tile rows.
+template <int CG, int BN>
+struct LinCfg {
+  static constexpr int kStages = CG == 2 ? 5 : 5;
+  static constexpr int kBRows = BN / CG;  // rows of w a CTA loads
+  static constexpr uint32_t kABytes = 128 * 128, kBBytes = kBRows * 128;
+  static constexpr uint32_t kSaBytes = 2048, kSbBytes = BN / 128 * 2048;  // MXFP4 uses half
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
+  static constexpr uint32_t kOutBytes = 4096;  // 32 rows x 128 bytes, two per epilogue warp
+  static constexpr uint32_t kOutOff = kStages * kStageBytes;
+  static constexpr uint32_t kColOff = kOutOff + 8 * kOutBytes;  // [2][BN] fp32: row scales of w, bias
+  static constexpr uint32_t kBarOff = kColOff + 2 * BN * 4;
+  static constexpr uint32_t kSmem = 1024 + kBarOff + 256;
+  static constexpr uint32_t kAcc1 = BN == 256 ? 192 : BN;        // TMEM column of the second accumulator
+  static constexpr uint32_t kSfCol = kAcc1 + BN;                 // scale slots: 4 columns of x, BN / 32 of w
+  static constexpr uint32_t kSfCols = 4 + BN / 32;
+  static constexpr int kSfSlots = 5;
+  static_assert(kSfCol + kSfSlots * kSfCols <= 512, "TMEM columns");
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+// Bounded wait of a whole warp, which leaves it together.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int *status, volatile int *abort_flag) {
   const bool ok = mbar_wait(bar, parity, status, abort_flag);
   return __all_sync(0xffffffffu, ok);
 }
 
-struct LinCfg {
-  static constexpr int kStages = 5;
-  static constexpr uint32_t kABytes = 128 * 128, kBBytes = 128 * 128;
-  static constexpr uint32_t kSfBytes = 2048;  // 128 rows x 256 columns of scales (MXFP4 uses half)
-  static constexpr uint32_t kStageBytes = kABytes + kBBytes + 2 * kSfBytes;
-  static constexpr uint32_t kOutBytes = 4096;  // 32 rows x 128 bytes, two per epilogue warp
-  static constexpr uint32_t kOutOff = kStages * kStageBytes;
-  static constexpr uint32_t kColOff = kOutOff + 8 * kOutBytes;  // [2][2][128] fp32 row scales of w, bias
-  static constexpr uint32_t kBarOff = kColOff + 2 * 2 * 128 * 4;
-  static constexpr uint32_t kSmem = 1024 + kBarOff + 256;
-  static constexpr uint32_t kSfCol = 256;  // TMEM columns past the two accumulators
-};
-
-// GELU, tanh form, as u * sigmoid(2 z) with the exact exponential identity
-// (1 + tanh z) / 2 = 1 / (1 + e^(-2z)); relative error a few 2^-22.
-__device__ __forceinline__ float gelu_exact(float u) {
+// GELU, tanh form, as u * sigmoid(2 z) by the identity (1 + tanh z) / 2 =
+// 1 / (1 + e^(-2z)); relative error a few 2^-22.
+__device__ __forceinline__ float gelu_sigmoid(float u) {
   const float z2 = 1.5957691216057308f * fmaf(0.044715f * u, u * u, u);  // 2 sqrt(2/pi) (...)
   return __fdividef(u, 1.f + exp2_approx(-1.4426950408889634f * z2));
 }
 
-template <int FMT>
+// 64 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float *v) {
+  tmem_ld32_async(taddr, v);
+  tmem_ld32_async(taddr + 32, v + 32);
+  tmem_wait_ld_regs(v);
+  reg_fence32(v + 32);
+}
+
+template <int FMT, int CG, int BN>
 __global__ void __launch_bounds__(192, 1)
-    linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                      const __grid_constant__ CUtensorMap tm_out, const LinearFp4Params p) {
-  using C = LinCfg;
+    linear_fp4_kernel(const __grid_constant__ LinearFp4Maps m, const LinearFp4Params p) {
+  using C = LinCfg<CG, BN>;
   constexpr int S = C::kStages;
   constexpr bool S16 = FMT == kNvfp4;
-  constexpr int kAtoms = S16 ? 4 : 2;  // 512-byte scale tiles per stage and operand
+  constexpr int kAtoms = S16 ? 4 : 2;       // scale tiles per stage and 128 rows
+  constexpr int kPerAtom = 4 / kAtoms;      // MMAs (64 columns of K) per scale tile
+  constexpr uint32_t kTx = CG * (C::kABytes + C::kBBytes + kAtoms * 512 * (1 + BN / 128));
+  constexpr int kEpiArrivals = 4 * CG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align_up<1024>(smem_raw);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
   uint64_t *empty = full + S;
   uint64_t *acc_full = empty + S;      // [2]
   uint64_t *acc_empty = acc_full + 2;  // [2]
-  uint64_t *col_bar = acc_empty + 2;   // the epilogue's per-column values of a tile are in place
+  uint64_t *shared_empty = acc_empty + 2;  // the columns both accumulators share are drained
+  uint64_t *col_bar = shared_empty + 1;    // the epilogue warps of this CTA
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(col_bar + 1);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  uint32_t *go = tmem_slot + 1;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (*(volatile int *)p.status != kDevOk) return;
-  const int tiles_m = (p.T + 127) / 128, tiles_n = (p.N + 127) / 128;
+  const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
+  const int tiles_m = (p.T + 128 * CG - 1) / (128 * CG), tiles_n = (p.N + BN - 1) / BN;
   const int ntiles = tiles_m * tiles_n;
+  const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
   const int nk = (p.K + 255) / 256;
-  const int64_t sf_tiles = static_cast<int64_t>(nk) * kAtoms;
+  const int sf_rows = nk * kAtoms;  // scale tiles along the columns
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -76,165 +106,269 @@ __global__ void __launch_bounds__(192, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&acc_full[s], 1);
-      mbar_init(&acc_empty[s], 128);
+      mbar_init(&acc_empty[s], kEpiArrivals);
     }
-    mbar_init(col_bar, 128);
+    mbar_init(shared_empty, kEpiArrivals);
+    mbar_init(col_bar, 4);
     *abort_flag = 0;
+    *go = *(volatile int *)p.status == kDevOk;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    if (CG == 2) {
+      tmem_alloc_pair(tmem_slot, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
+  // both CTAs of a pair go by the leader's reading of the status word
+  const bool run = (CG == 2 ? cluster_load(cluster_addr(go, 0)) : *go) != 0;
 
-  if (warp == 0) {
+  if (!run) {
+  } else if (warp == 0 && lane == 0) {
     int kg = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+    for (int tile = first; tile < ntiles && ok; tile += step) {
       const int mt = tile / tiles_n, nt = tile - mt * tiles_n;
+      const int xr = mt * CG + rank;  // this CTA's 128 rows of x
       for (int kb = 0; kb < nk; ++kb, ++kg) {
         const int s = kg % S;
-        if (!wait_warp(&empty[s], ((kg / S) & 1) ^ 1, p.status, abort_flag)) {
+        if (!mbar_wait(&empty[s], ((kg / S) & 1) ^ 1, p.status, abort_flag)) {
           ok = false;
           break;
         }
-        if (lane == 0) {
-          uint8_t *st = smem + s * C::kStageBytes;
-          mbar_arrive_expect_tx(&full[s], C::kABytes + C::kBBytes + 2 * kAtoms * 512);
-          tma_load_2d(st, &tm_x, &full[s], kb * 128, mt * 128);
-          tma_load_2d(st + C::kABytes, &tm_w, &full[s], kb * 128, nt * 128);
-          bulk_load(st + C::kABytes + C::kBBytes, p.sx + (mt * sf_tiles + kb * kAtoms) * 512, kAtoms * 512, &full[s]);
-          bulk_load(st + C::kABytes + C::kBBytes + C::kSfBytes, p.sw + (nt * sf_tiles + kb * kAtoms) * 512,
-                    kAtoms * 512, &full[s]);
+        uint8_t *a = smem + s * C::kStageBytes, *b = a + C::kABytes, *sa = b + C::kBBytes, *sb = sa + C::kSaBytes;
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], kTx);
+        if (CG == 2) {
+          const uint32_t bar = cluster_addr(&full[s], 0);
+          tma_load_2d_pair(a, &m.x, bar, kb * 128, xr * 128);
+          tma_load_2d_pair(b, &m.w, bar, kb * 128, nt * BN + rank * C::kBRows);
+          tma_load_2d_pair(sa, &m.sx, bar, 0, xr * sf_rows + kb * kAtoms);
+#pragma unroll
+          for (int i = 0; i < BN / 128; ++i)
+            tma_load_2d_pair(sb + i * kAtoms * 512, &m.sw, bar, 0, (nt * (BN / 128) + i) * sf_rows + kb * kAtoms);
+        } else {
+          tma_load_2d(a, &m.x, &full[s], kb * 128, xr * 128);
+          tma_load_2d(b, &m.w, &full[s], kb * 128, nt * BN);
+          tma_load_2d(sa, &m.sx, &full[s], 0, xr * sf_rows + kb * kAtoms);
+          tma_load_2d(sb, &m.sw, &full[s], 0, nt * sf_rows + kb * kAtoms);
         }
-        __syncwarp();
       }
     }
-    if (!ok)  // gave up: let the copies in flight land before the CTA's shared memory goes away
+    if (!ok && rank == 0)  // gave up: let the copies in flight land before the shared memory goes away
       for (int f = max(kg - S, 0); f < kg; ++f) mbar_drain(&full[f % S], (f / S) & 1);
-  } else if (warp == 1) {
-    int kg = 0, tl = 0;
-    bool ok = true;
-    const uint32_t sfa = tmem + C::kSfCol, sfb = sfa + 16;
-    for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x, ++tl) {
-      const int ab = tl & 1;
-      if (!wait_warp(&acc_empty[ab], ((tl >> 1) & 1) ^ 1, p.status, abort_flag)) break;
+  } else if (warp == 1 && rank == 0) {
+    const uint32_t lead = elect_lane();
+    const int my_tiles = first < ntiles ? (ntiles - 1 - first) / step + 1 : 0;
+    const int stages = my_tiles * nk;
+    const uint32_t sf = tmem + C::kSfCol;
+    int slot = 0;                      // scale slot of the next copy
+    // copies scale tile j of stage kg into the next slot; returns the slot's columns
+    auto copy_scales = [&](int kg, int j) {
+      const uint32_t f0 = smem_u32(smem + (kg % S) * C::kStageBytes + C::kABytes + C::kBBytes) + 512 * j;
+      const uint32_t at = sf + slot * C::kSfCols;
+      tmem_cp_scales<CG>(at, sdesc_plain(f0), lead);
+#pragma unroll
+      for (int i = 0; i < BN / 128; ++i)
+        tmem_cp_scales<CG>(at + 4 + 4 * i, sdesc_plain(f0 + C::kSaBytes + i * kAtoms * 512), lead);
+      slot = slot + 1 == C::kSfSlots ? 0 : slot + 1;
+      return at;
+    };
+    bool ok = stages > 0 && wait_warp(&full[0], 0, p.status, abort_flag);
+    uint32_t next = 0;
+    if (ok) {
       tc_fence_after();
-      for (int kb = 0; kb < nk; ++kb, ++kg) {
-        const int s = kg % S;
-        if (!wait_warp(&full[s], (kg / S) & 1, p.status, abort_flag)) {
-          ok = false;
-          break;
+      next = copy_scales(0, 0);
+    }
+    int kg = 0;
+    for (int tl = 0; tl < my_tiles && ok; ++tl) {
+      const int ab = tl & 1;
+      const uint32_t acc = tmem + ab * C::kAcc1;
+      ok = wait_warp(&acc_empty[ab], ((tl >> 1) & 1) ^ 1, p.status, abort_flag);
+      if (BN == 256 && ok && tl > 0) ok = wait_warp(shared_empty, (tl - 1) & 1, p.status, abort_flag);
+      tc_fence_after();
+      for (int kb = 0; kb < nk && ok; ++kb, ++kg) {
+        const uint32_t a0 = smem_u32(smem + (kg % S) * C::kStageBytes), b0 = a0 + C::kABytes;
+#pragma unroll
+        for (int j = 0; j < kAtoms && ok; ++j) {
+          const uint32_t sa = next, sb = sa + 4;
+          if (j + 1 < kAtoms) {
+            next = copy_scales(kg, j + 1);
+          } else if (kg + 1 < stages) {
+            ok = wait_warp(&full[(kg + 1) % S], ((kg + 1) / S) & 1, p.status, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            next = copy_scales(kg + 1, 0);
+          }
+#pragma unroll
+          for (int q = 0; q < kPerAtom; ++q) {
+            const int kk = j * kPerAtom + q;
+            umma_fp4<S16, CG>(acc, sdesc_sw128(a0 + kk * 32, 16, 1024), sdesc_sw128(b0 + kk * 32, 16, 1024),
+                              idesc_fp4(128 * CG, BN, S16, q * 2), sa, sb, (kb | kk) != 0, lead);
+          }
         }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t a0 = smem_u32(smem + s * C::kStageBytes);
-          const uint32_t b0 = a0 + C::kABytes, f0 = b0 + C::kBBytes, g0 = f0 + C::kSfBytes;
-#pragma unroll
-          for (int j = 0; j < kAtoms; ++j) {
-            tmem_cp_scales(sfa + 4 * j, sdesc_plain(f0 + 512 * j));
-            tmem_cp_scales(sfb + 4 * j, sdesc_plain(g0 + 512 * j));
+        if (!ok) break;
+        if (lead) {
+          if (CG == 2) {
+            umma_commit_pair(&empty[kg % S]);
+            if (kb == nk - 1) umma_commit_pair(&acc_full[ab]);
+          } else {
+            umma_commit(&empty[kg % S]);
+            if (kb == nk - 1) umma_commit(&acc_full[ab]);
           }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const int j = S16 ? kk : kk >> 1;
-            umma_fp4<S16>(tmem + ab * 128, sdesc_sw128(a0 + kk * 32, 16, 1024), sdesc_sw128(b0 + kk * 32, 16, 1024),
-                          idesc_fp4(128, 128, S16, S16 ? 0 : (kk & 1) * 2), sfa + 4 * j, sfb + 4 * j,
-                          (kb | kk) != 0);
-          }
-          umma_commit(&empty[s]);
-          if (kb == nk - 1) umma_commit(&acc_full[ab]);
         }
         __syncwarp();
       }
     }
-  } else {
+  } else if (warp >= 2) {
     const int quad = warp & 3;  // TMEM lanes this warp may read
     const int e = threadIdx.x - 64;
     uint8_t *stage = smem + C::kOutOff + (warp - 2) * 2 * C::kOutBytes;
-    float *cols = reinterpret_cast<float *>(smem + C::kColOff);
+    float *rw = reinterpret_cast<float *>(smem + C::kColOff), *bs = rw + BN;
     int tl = 0, buf = 0;
-    for (int tile = blockIdx.x; tile < ntiles; tile += gridDim.x, ++tl) {
+    // a drained accumulator (or its shared columns) goes back to the leader's MMA thread
+    auto release = [&](uint64_t *bar) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          mbar_arrive_cluster(cluster_addr(bar, 0));
+        else
+          mbar_arrive(bar);
+      }
+    };
+    for (int tile = first; tile < ntiles; tile += step, ++tl) {
       const int mt = tile / tiles_n, nt = tile - mt * tiles_n;
       const int ab = tl & 1;
-      // this tile's per-column factors and biases (double-buffered by tile), this thread's row factor
-      float *rw = cols + ab * 256, *bs = rw + 128;
-      const int n = nt * 128 + e;
-      rw[e] = S16 && n < p.N ? p.rw[n] : 1.f;
-      bs[e] = p.bias != nullptr && n < p.N ? bf16_bits_to_f32(p.bias[n]) : 0.f;
-      const int row = mt * 128 + quad * 32 + lane;
-      const float rx = S16 && row < p.T ? p.rx[row] : 1.f;
-      mbar_arrive(col_bar);
-      if (!wait_warp(col_bar, tl & 1, p.status, abort_flag)) break;
+      const int row0 = (mt * CG + rank) * 128 + quad * 32;
+      const float rx = S16 && row0 + lane < p.T ? p.rx[row0 + lane] : 1.f;
+      // the warps have read the previous tile's column values; put this tile's in place
+      if (lane == 0) mbar_arrive(col_bar);
+      if (!wait_warp(col_bar, 0, p.status, abort_flag)) break;
+#pragma unroll
+      for (int c = e; c < BN; c += 128) {
+        const int n = nt * BN + c;
+        rw[c] = S16 && n < p.N ? p.rw[n] : 1.f;
+        bs[c] = p.bias != nullptr && n < p.N ? bf16_bits_to_f32(p.bias[n]) : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(col_bar);
+      if (!wait_warp(col_bar, 1, p.status, abort_flag)) break;
       if (!wait_warp(&acc_full[ab], (tl >> 1) & 1, p.status, abort_flag)) break;
       tc_fence_after();
-      const int chunk = p.out_f32 ? 32 : 64;  // columns of one 128-byte store row
-      for (int c0 = 0; c0 < 128; c0 += chunk) {
-        uint8_t *dst = stage + buf * C::kOutBytes;
-        if (lane == 0) bulk_wait_read<1>();  // the store that used this buffer has read it
-        __syncwarp();
-        for (int c1 = 0; c1 < chunk; c1 += 32) {
-          float v[32];
-          tmem_ld32(tmem + ab * 128 + (static_cast<uint32_t>(quad * 32) << 16) + c0 + c1, v);
+      constexpr int kChunks = BN / 64;
+      for (int i = 0; i < kChunks; ++i) {
+        // columns shared by both accumulators first: the last 64 of the first one, the first 64 of the second
+        const int c0 = ((BN == 256 && ab == 0 ? kChunks - 1 : 0) + i) % kChunks * 64;
+        float v[64];
+        tmem_ld64(tmem + ab * C::kAcc1 + (static_cast<uint32_t>(quad * 32) << 16) + c0, v);
+        if (BN == 256 && i == 0) release(shared_empty);
+        if (i == kChunks - 1) release(&acc_empty[ab]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            v[i] = fmaf(v[i], rx * rw[c0 + c1 + i], bs[c0 + c1 + i]);
-            if (p.gelu) v[i] = gelu_exact(v[i]);
+        for (int q = 0; q < 64; q += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(rw + c0 + q);
+          const float4 g = *reinterpret_cast<const float4 *>(bs + c0 + q);
+          v[q] = fmaf(v[q], rx * f.x, g.x);
+          v[q + 1] = fmaf(v[q + 1], rx * f.y, g.y);
+          v[q + 2] = fmaf(v[q + 2], rx * f.z, g.z);
+          v[q + 3] = fmaf(v[q + 3], rx * f.w, g.w);
+        }
+        if (p.gelu) {
+#pragma unroll
+          for (int q = 0; q < 64; ++q) v[q] = gelu_sigmoid(v[q]);
+        }
+        const int x0 = nt * BN + c0;
+        auto store = [&](const uint8_t *src, int x) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (x < p.N && row0 < p.T) tma_store_2d(&m.out, src, x, row0);
+            bulk_commit();
           }
-          if (p.out_f32) {
+          buf ^= 1;
+        };
+        auto buffer = [&]() {  // the store that used this buffer has read it
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+          return stage + buf * C::kOutBytes;
+        };
+        if (p.out_f32) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint8_t *dst = buffer();
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<float4 *>(dst + sw128_offset(lane, q)) =
-                  make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4 *>(dst + sw128_offset(lane, c1 / 8 + q)) =
-                  make_uint4(cvt_bf16x2(v[8 * q], v[8 * q + 1]), cvt_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                             cvt_bf16x2(v[8 * q + 4], v[8 * q + 5]), cvt_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+              *reinterpret_cast<float4 *>(dst + sw128_offset(lane, q)) = make_float4(
+                  v[32 * hf + 4 * q], v[32 * hf + 4 * q + 1], v[32 * hf + 4 * q + 2], v[32 * hf + 4 * q + 3]);
+            store(dst, x0 + 32 * hf);
           }
+        } else {
+          uint8_t *dst = buffer();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4 *>(dst + sw128_offset(lane, q)) =
+                make_uint4(cvt_bf16x2(v[8 * q], v[8 * q + 1]), cvt_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                           cvt_bf16x2(v[8 * q + 4], v[8 * q + 5]), cvt_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+          store(dst, x0);
         }
-        if (c0 + chunk >= 128) {  // the accumulator is read out
-          tc_fence_before();
-          mbar_arrive(&acc_empty[ab]);
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (nt * 128 + c0 < p.N && mt * 128 + quad * 32 < p.T)
-            tma_store_2d(&tm_out, dst, nt * 128 + c0, mt * 128 + quad * 32);
-          bulk_commit();
-        }
-        buf ^= 1;
       }
     }
     if (lane == 0) bulk_wait_all();
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync();  // neither CTA's memory goes away while the other still uses it
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) {
+    if (CG == 2)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int CG, int BN>
+cudaError_t launch_form(const LinearFp4Params &p, LinearFp4Maps m, int sms, cudaStream_t s) {
+  using C = LinCfg<CG, BN>;
+  const int64_t tiles = static_cast<int64_t>((p.T + 128 * CG - 1) / (128 * CG)) * ((p.N + BN - 1) / BN);
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(tiles, sms / CG)) * CG;
+  auto kernel = p.fmt == kNvfp4 ? linear_fp4_kernel<kNvfp4, CG, BN> : linear_fp4_kernel<kMxfp4, CG, BN>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, m, p);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_fp4(const LinearFp4Params &p, const CUtensorMap &tm_x, const CUtensorMap &tm_w,
-                              const CUtensorMap &tm_out, cudaStream_t s) {
-  const int64_t tiles = static_cast<int64_t>((p.T + 127) / 128) * ((p.N + 127) / 128);
+cudaError_t launch_linear_fp4(const LinearFp4Params &p, const LinearFp4Maps &m, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(tiles, sms));
-  auto kernel = p.fmt == kNvfp4 ? linear_fp4_kernel<kNvfp4> : linear_fp4_kernel<kMxfp4>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LinCfg::kSmem);
-  if (e != cudaSuccess) return e;
-  kernel<<<blocks, 192, LinCfg::kSmem, s>>>(tm_x, tm_w, tm_out, p);
-  return cudaGetLastError();
+  // waves of the pair form and of the single form, whose wave takes about half as long
+  const int64_t pair = static_cast<int64_t>((p.T + 255) / 256) * ((p.N + 255) / 256);
+  const int64_t single = static_cast<int64_t>((p.T + 127) / 128) * ((p.N + 127) / 128);
+  const int64_t pair_waves = (pair + sms / 2 - 1) / (sms / 2), single_waves = (single + sms - 1) / sms;
+  return 2 * pair_waves <= single_waves ? launch_form<2, 256>(p, m, sms, s) : launch_form<1, 128>(p, m, sms, s);
 }
 
 }  // namespace cm
