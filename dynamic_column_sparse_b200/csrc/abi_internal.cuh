@@ -18,10 +18,10 @@ chipmunk_status record_errorf(chipmunk_status st, const char *fmt, ...) __attrib
 // Checks that the current device is sm_100 and resolves its status word.
 chipmunk_status device_ready(int **status_out);
 
-// Rank-2 tensor map (128-byte swizzle or none) over rows x cols elements, row-major with
-// `pitch` bytes between rows; box = box_cols x box_rows.
-chipmunk_status encode_map2d(CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t rows, uint64_t cols,
-                             uint64_t pitch, uint32_t box_cols, uint32_t box_rows, bool swizzled, const char *what);
+// Tensor map of rank 2 or 3 (128-byte swizzle or none); dims, strides (from the
+// second dimension on, in bytes) and box innermost first.
+chipmunk_status encode_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, int rank, const uint64_t *dims,
+                           const uint64_t *strides, const uint32_t *box, bool swizzled, const char *what);
 
 // chipmunk_mlp_delta with its delta scratch taken from get_scratch instead of
 // a caller workspace. The arguments are checked first; a step that needs more

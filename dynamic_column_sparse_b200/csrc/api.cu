@@ -296,11 +296,13 @@ chipmunk_status record_errorf(chipmunk_status st, const char *fmt, ...) {
 
 chipmunk_status device_ready(int **status_out) { return device_setup(status_out); }
 
-chipmunk_status encode_map2d(CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t rows, uint64_t cols,
-                             uint64_t pitch, uint32_t box_cols, uint32_t box_rows, bool swizzled, const char *what) {
-  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
-  const cuuint32_t box[2] = {box_cols, box_rows}, es[2] = {1, 1};
-  CUresult r = g_encode(m, type, 2, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+chipmunk_status encode_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, int rank, const uint64_t *dims,
+                           const uint64_t *strides, const uint32_t *box, bool swizzled, const char *what) {
+  cuuint64_t gd[3], gs[2];
+  cuuint32_t bx[3], es[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) gd[i] = dims[i], bx[i] = box[i];
+  for (int i = 0; i < rank - 1; ++i) gs[i] = strides[i];
+  CUresult r = g_encode(m, type, rank, const_cast<void *>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(CHIPMUNK_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, int(r));

@@ -84,6 +84,30 @@ chipmunk_fp4_rows ws_rows(const chipmunk_linear_fp4_args *a, void *ws) {
   return {a->T, a->w.cols, a->w.format, p, p + codes, reinterpret_cast<float *>(p + codes + scales)};
 }
 
+// Tensor maps of a linear call. Codes: rows of bytes, boxes of 128 bytes (256 columns) x 128
+// rows. Block scales: 512-byte tiles as 128 words, boxes of the tiles of 256 columns of
+// one row tile of x and of as many of w as the product's tile has. out: boxes of 128 bytes x 32 rows.
+chipmunk_status linear_maps(cm::LinearFp4Maps *m, const chipmunk_linear_fp4_args *a, const chipmunk_fp4_rows &xq) {
+  const uint64_t T = a->T, N = a->N, bytes = uint64_t(a->w.cols) / 2;
+  const uint64_t tiles = cm::fp4_scale_tiles(a->w.cols, a->w.format);
+  const uint32_t per_stage = a->w.format == CHIPMUNK_NVFP4 ? 4 : 2;
+  const bool f32 = a->out_type == CHIPMUNK_FP32;
+  const uint64_t out_es = f32 ? 4 : 2;
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, i32 = CU_TENSOR_MAP_DATA_TYPE_INT32;
+  const uint64_t dx[] = {bytes, T}, dw[] = {bytes, N}, dsx[] = {128, tiles, (T + 127) / 128},
+                 dsw[] = {128, tiles, (N + 127) / 128}, dout[] = {N, T};
+  const uint64_t sb[] = {bytes}, ss[] = {512, tiles * 512}, so[] = {N * out_es};
+  const uint32_t box[] = {128, 128}, bsx[] = {128, per_stage, 1}, bsw1[] = {128, per_stage, 1},
+                 bsw2[] = {128, per_stage, 2}, bout[] = {uint32_t(128 / out_es), 32};
+  CM_CHECK(cm::encode_map(&m->x, u8, xq.codes, 2, dx, sb, box, true, "x codes"));
+  CM_CHECK(cm::encode_map(&m->w, u8, a->w.codes, 2, dw, sb, box, true, "w codes"));
+  CM_CHECK(cm::encode_map(&m->sx, i32, xq.scales, 3, dsx, ss, bsx, false, "x scales"));
+  m->pair = cm::linear_fp4_pair(T, N);
+  CM_CHECK(cm::encode_map(&m->sw, i32, a->w.scales, 3, dsw, ss, m->pair ? bsw2 : bsw1, false, "w scales"));
+  return cm::encode_map(&m->out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->out, 2,
+                        dout, so, bout, true, "out");
+}
+
 }  // namespace
 
 namespace cm {
@@ -166,20 +190,9 @@ chipmunk_status chipmunk_linear_fp4(const chipmunk_linear_fp4_args *a, void *ws,
   int *status = nullptr;
   CM_CHECK(cm::device_ready(&status));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const uint64_t row_bytes = uint64_t(a->w.cols) / 2;
   const bool f32 = a->out_type == CHIPMUNK_FP32;
   cm::LinearFp4Maps m;
-  const CUtensorMapDataType bytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  CM_CHECK(cm::encode_map2d(&m.x, bytes, xq.codes, a->T, row_bytes, row_bytes, 128, 128, true, "x codes"));
-  CM_CHECK(cm::encode_map2d(&m.w, bytes, a->w.codes, a->N, row_bytes, row_bytes, 128, 128, true, "w codes"));
-  const uint64_t tiles = cm::fp4_scale_tiles(a->w.cols, a->w.format);
-  const uint32_t per_stage = a->w.format == CHIPMUNK_NVFP4 ? 4 : 2;
-  CM_CHECK(cm::encode_map2d(&m.sx, CU_TENSOR_MAP_DATA_TYPE_INT32, xq.scales, (a->T + 127) / 128 * tiles, 128, 512, 128,
-                            per_stage, false, "x scales"));
-  CM_CHECK(cm::encode_map2d(&m.sw, CU_TENSOR_MAP_DATA_TYPE_INT32, a->w.scales, (a->N + 127) / 128 * tiles, 128, 512,
-                            128, per_stage, false, "w scales"));
-  CM_CHECK(cm::encode_map2d(&m.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->out,
-                            a->T, a->N, uint64_t(a->N) * (f32 ? 4 : 2), f32 ? 32 : 64, 32, true, "out"));
+  CM_CHECK(linear_maps(&m, a, xq));
   if (a->x != nullptr)
     CM_CUDA(cm::launch_quantize_fp4_rows(quant_params(a->x, &xq, status), s), "4-bit quantise launch");
   cm::LinearFp4Params p{int(a->T),

@@ -150,12 +150,15 @@ struct LinearFp4Params {
   const uint16_t *bias;        // [N] bf16 or nullptr
   int *status;
 };
-// Byte maps over the codes (boxes of 128 bytes x 128 rows), maps over the block
-// scales as rows of 128 words, one 512-byte scale tile each (boxes of one stage's tiles of
-// 128 rows), and a map over out (boxes of 128 bytes x 32 rows).
+// Codes as rows of bytes (boxes of 128 bytes x 128 rows); block scales as 512-byte
+// tiles, [tiles of 128 rows][tiles along the columns][128 words] (boxes of one
+// stage's tiles of one row tile of x, of one or two row tiles of w); out (boxes of 128 bytes x 32
+// rows). pair: the maps are those of the form of the kernel that works in CTA pairs.
 struct LinearFp4Maps {
   CUtensorMap x, w, sx, sw, out;
+  bool pair;
 };
+bool linear_fp4_pair(int64_t T, int64_t N);  // which form a product of these sizes takes
 cudaError_t launch_linear_fp4(const LinearFp4Params &p, const LinearFp4Maps &m, cudaStream_t s);
 
 // ------------------------------------------------------------------ norms with gate and residual

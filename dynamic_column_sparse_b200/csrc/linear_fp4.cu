@@ -14,7 +14,7 @@
 // copies scales to TMEM and issues the MMAs. The scale columns are a ring of
 // their own, one slot per scale tile, filled one slot ahead of the MMAs: with a
 // copy and its MMAs back to back the tensor core idled more than half the time
-// (546 of 1240 cycles per stage busy, ncu). Warps 2-5 drain one accumulator (scales,
+// (546 of 1240 cycles per stage busy, ncu). Warps 2-9 drain one accumulator (scales,
 // bias, activation, rounding, TMA stores through swizzled shared memory) while
 // the other is being filled. At 256 columns the two accumulators share 64 TMEM
 // columns, which leaves 64 for the scales: the shared columns are drained first and the next
@@ -36,7 +36,7 @@ struct LinCfg {
   static constexpr uint32_t kABytes = 128 * 128, kBBytes = kBRows * 128;
   static constexpr uint32_t kSaBytes = 2048, kSbBytes = BN / 128 * 2048;  // MXFP4 uses half
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
-  static constexpr uint32_t kOutBytes = 4096;  // 32 rows x 128 bytes, two per epilogue warp
+  static constexpr uint32_t kOutBytes = 4096;  // 32 rows x 128 bytes, one per epilogue warp
   static constexpr uint32_t kOutOff = kStages * kStageBytes;
   static constexpr uint32_t kColOff = kOutOff + 8 * kOutBytes;  // [2][BN] fp32: row scales of w, bias
   static constexpr uint32_t kBarOff = kColOff + 2 * BN * 4;
@@ -51,6 +51,7 @@ struct LinCfg {
 
 // Bounded wait of a whole warp, which leaves it together.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int *status, volatile int *abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const bool ok = mbar_wait(bar, parity, status, abort_flag);
   return __all_sync(0xffffffffu, ok);
 }
@@ -71,7 +72,7 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float *v) {
 }
 
 template <int FMT, int CG, int BN>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(320, 1)
     linear_fp4_kernel(const __grid_constant__ LinearFp4Maps m, const LinearFp4Params p) {
   using C = LinCfg<CG, BN>;
   constexpr int S = C::kStages;
@@ -79,7 +80,7 @@ __global__ void __launch_bounds__(192, 1)
   constexpr int kAtoms = S16 ? 4 : 2;       // scale tiles per stage and 128 rows
   constexpr int kPerAtom = 4 / kAtoms;      // MMAs (64 columns of K) per scale tile
   constexpr uint32_t kTx = CG * (C::kABytes + C::kBBytes + kAtoms * 512 * (1 + BN / 128));
-  constexpr int kEpiArrivals = 4 * CG;
+  constexpr int kEpiArrivals = 8 * CG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align_up<1024>(smem_raw);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
@@ -97,7 +98,6 @@ __global__ void __launch_bounds__(192, 1)
   const int ntiles = tiles_m * tiles_n;
   const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
   const int nk = (p.K + 255) / 256;
-  const int sf_rows = nk * kAtoms;  // scale tiles along the columns
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(192, 1)
       mbar_init(&acc_full[s], 1);
       mbar_init(&acc_empty[s], kEpiArrivals);
     }
-    mbar_init(shared_empty, kEpiArrivals);
-    mbar_init(col_bar, 4);
+    mbar_init(shared_empty, kEpiArrivals / 2);
+    mbar_init(col_bar, 8);
     *abort_flag = 0;
     *go = *(volatile int *)p.status == kDevOk;
     fence_barrier_init();
@@ -132,34 +132,27 @@ __global__ void __launch_bounds__(192, 1)
   const bool run = (CG == 2 ? cluster_load(cluster_addr(go, 0)) : *go) != 0;
 
   if (!run) {
-  } else if (warp == 0 && lane == 0) {
-    int kg = 0;
+  } else if (warp == 0) {
+    const uint32_t lead = elect_lane();
+    int s = 0, kg = 0;
+    uint32_t ph = 1;  // parity of the wait for an empty stage
     bool ok = true;
     for (int tile = first; tile < ntiles && ok; tile += step) {
       const int mt = tile / tiles_n, nt = tile - mt * tiles_n;
       const int xr = mt * CG + rank;  // this CTA's 128 rows of x
       for (int kb = 0; kb < nk; ++kb, ++kg) {
-        const int s = kg % S;
-        if (!mbar_wait(&empty[s], ((kg / S) & 1) ^ 1, p.status, abort_flag)) {
+        if (!wait_warp(&empty[s], ph, p.status, abort_flag)) {
           ok = false;
           break;
         }
         uint8_t *a = smem + s * C::kStageBytes, *b = a + C::kABytes, *sa = b + C::kBBytes, *sb = sa + C::kSaBytes;
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], kTx);
-        if (CG == 2) {
-          const uint32_t bar = cluster_addr(&full[s], 0);
-          tma_load_2d_pair(a, &m.x, bar, kb * 128, xr * 128);
-          tma_load_2d_pair(b, &m.w, bar, kb * 128, nt * BN + rank * C::kBRows);
-          tma_load_2d_pair(sa, &m.sx, bar, 0, xr * sf_rows + kb * kAtoms);
-#pragma unroll
-          for (int i = 0; i < BN / 128; ++i)
-            tma_load_2d_pair(sb + i * kAtoms * 512, &m.sw, bar, 0, (nt * (BN / 128) + i) * sf_rows + kb * kAtoms);
-        } else {
-          tma_load_2d(a, &m.x, &full[s], kb * 128, xr * 128);
-          tma_load_2d(b, &m.w, &full[s], kb * 128, nt * BN);
-          tma_load_2d(sa, &m.sx, &full[s], 0, xr * sf_rows + kb * kAtoms);
-          tma_load_2d(sb, &m.sw, &full[s], 0, nt * sf_rows + kb * kAtoms);
-        }
+        if (CG == 1 || rank == 0) mbar_arrive_expect_tx_lead(&full[s], kTx, lead);
+        const uint32_t bar = CG == 2 ? cluster_addr(&full[s], 0) : smem_u32(&full[s]);
+        tma_load_2d_lead<CG>(a, &m.x, bar, kb * 128, xr * 128, lead);
+        tma_load_2d_lead<CG>(b, &m.w, bar, kb * 128, nt * BN + rank * C::kBRows, lead);
+        tma_load_3d_lead<CG>(sa, &m.sx, bar, 0, kb * kAtoms, xr, lead);
+        tma_load_3d_lead<CG>(sb, &m.sw, bar, 0, kb * kAtoms, nt * (BN / 128), lead);
+        if (++s == S) s = 0, ph ^= 1;
       }
     }
     if (!ok && rank == 0)  // gave up: let the copies in flight land before the shared memory goes away
@@ -167,73 +160,74 @@ __global__ void __launch_bounds__(192, 1)
   } else if (warp == 1 && rank == 0) {
     const uint32_t lead = elect_lane();
     const int my_tiles = first < ntiles ? (ntiles - 1 - first) / step + 1 : 0;
-    const int stages = my_tiles * nk;
-    const uint32_t sf = tmem + C::kSfCol;
-    int slot = 0;                      // scale slot of the next copy
-    // copies scale tile j of stage kg into the next slot; returns the slot's columns
-    auto copy_scales = [&](int kg, int j) {
-      const uint32_t f0 = smem_u32(smem + (kg % S) * C::kStageBytes + C::kABytes + C::kBBytes) + 512 * j;
-      const uint32_t at = sf + slot * C::kSfCols;
-      tmem_cp_scales<CG>(at, sdesc_plain(f0), lead);
+    int left = my_tiles * nk;          // stages not yet looked at
+    const uint64_t desc_ab = sdesc_sw128(smem_u32(smem), 16, 1024), desc_sf = sdesc_plain(smem_u32(smem));
+    constexpr uint32_t kSfOff = C::kABytes + C::kBBytes;
+    uint32_t sf = C::kSfCol;           // columns of the next scale slot
+    // copies scale tile j of stage s into the next slot; returns the slot's columns
+    auto copy_scales = [&](int s, int j) {
+      const uint64_t d = desc_sf + static_cast<uint64_t>((s * C::kStageBytes + kSfOff + 512 * j) >> 4);
+      const uint32_t at = sf;
+      tmem_cp_scales<CG>(tmem + at, d, lead);
 #pragma unroll
       for (int i = 0; i < BN / 128; ++i)
-        tmem_cp_scales<CG>(at + 4 + 4 * i, sdesc_plain(f0 + C::kSaBytes + i * kAtoms * 512), lead);
-      slot = slot + 1 == C::kSfSlots ? 0 : slot + 1;
-      return at;
+        tmem_cp_scales<CG>(tmem + at + 4 + 4 * i, d + ((C::kSaBytes + i * kAtoms * 512) >> 4), lead);
+      sf = at + C::kSfCols == C::kSfCol + C::kSfSlots * C::kSfCols ? C::kSfCol : at + C::kSfCols;
+      return tmem + at;
     };
-    bool ok = stages > 0 && wait_warp(&full[0], 0, p.status, abort_flag);
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = left > 0 && wait_warp(&full[0], 0, p.status, abort_flag);
     uint32_t next = 0;
     if (ok) {
       tc_fence_after();
       next = copy_scales(0, 0);
     }
-    int kg = 0;
     for (int tl = 0; tl < my_tiles && ok; ++tl) {
       const int ab = tl & 1;
       const uint32_t acc = tmem + ab * C::kAcc1;
       ok = wait_warp(&acc_empty[ab], ((tl >> 1) & 1) ^ 1, p.status, abort_flag);
       if (BN == 256 && ok && tl > 0) ok = wait_warp(shared_empty, (tl - 1) & 1, p.status, abort_flag);
       tc_fence_after();
-      for (int kb = 0; kb < nk && ok; ++kb, ++kg) {
-        const uint32_t a0 = smem_u32(smem + (kg % S) * C::kStageBytes), b0 = a0 + C::kABytes;
+      for (int kb = 0; kb < nk && ok; ++kb) {
+        const uint64_t da = desc_ab + static_cast<uint64_t>((s * C::kStageBytes) >> 4), db = da + (C::kABytes >> 4);
+        const int s1 = s + 1 == S ? 0 : s + 1;
+        const uint32_t ph1 = s1 == 0 ? ph ^ 1 : ph;
+        --left;
 #pragma unroll
-        for (int j = 0; j < kAtoms && ok; ++j) {
-          const uint32_t sa = next, sb = sa + 4;
+        for (int j = 0; j < kAtoms; ++j) {
+          const uint32_t sa = next;
           if (j + 1 < kAtoms) {
-            next = copy_scales(kg, j + 1);
-          } else if (kg + 1 < stages) {
-            ok = wait_warp(&full[(kg + 1) % S], ((kg + 1) / S) & 1, p.status, abort_flag);
+            next = copy_scales(s, j + 1);
+          } else if (left > 0) {
+            ok = wait_warp(&full[s1], ph1, p.status, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            next = copy_scales(kg + 1, 0);
+            next = copy_scales(s1, 0);
           }
 #pragma unroll
           for (int q = 0; q < kPerAtom; ++q) {
             const int kk = j * kPerAtom + q;
-            umma_fp4<S16, CG>(acc, sdesc_sw128(a0 + kk * 32, 16, 1024), sdesc_sw128(b0 + kk * 32, 16, 1024),
-                              idesc_fp4(128 * CG, BN, S16, q * 2), sa, sb, (kb | kk) != 0, lead);
+            umma_fp4<S16, CG>(acc, da + kk * 2, db + kk * 2, idesc_fp4(128 * CG, BN, S16, q * 2), sa, sa + 4,
+                              (kb | kk) != 0, lead);
           }
         }
         if (!ok) break;
-        if (lead) {
-          if (CG == 2) {
-            umma_commit_pair(&empty[kg % S]);
-            if (kb == nk - 1) umma_commit_pair(&acc_full[ab]);
-          } else {
-            umma_commit(&empty[kg % S]);
-            if (kb == nk - 1) umma_commit(&acc_full[ab]);
-          }
-        }
-        __syncwarp();
+        umma_commit_lead<CG>(&empty[s], lead);
+        if (kb == nk - 1) umma_commit_lead<CG>(&acc_full[ab], lead);
+        s = s1, ph = ph1;
       }
     }
   } else if (warp >= 2) {
+    // two warps per lane quadrant, each half of the tile's columns
+    constexpr int kCols = BN / 2, kChunks = kCols / 64;
     const int quad = warp & 3;  // TMEM lanes this warp may read
+    const int half = (warp - 2) >> 2;
     const int e = threadIdx.x - 64;
-    uint8_t *stage = smem + C::kOutOff + (warp - 2) * 2 * C::kOutBytes;
+    uint8_t *stage = smem + C::kOutOff + (warp - 2) * C::kOutBytes;
     float *rw = reinterpret_cast<float *>(smem + C::kColOff), *bs = rw + BN;
-    int tl = 0, buf = 0;
-    // a drained accumulator (or its shared columns) goes back to the leader's MMA thread
+    int tl = 0;
+    // a drained accumulator (or its shared columns) goes back to the leader's MMA warp
     auto release = [&](uint64_t *bar) {
       tc_fence_before();
       __syncwarp();
@@ -252,24 +246,24 @@ __global__ void __launch_bounds__(192, 1)
       // the warps have read the previous tile's column values; put this tile's in place
       if (lane == 0) mbar_arrive(col_bar);
       if (!wait_warp(col_bar, 0, p.status, abort_flag)) break;
-#pragma unroll
-      for (int c = e; c < BN; c += 128) {
-        const int n = nt * BN + c;
-        rw[c] = S16 && n < p.N ? p.rw[n] : 1.f;
-        bs[c] = p.bias != nullptr && n < p.N ? bf16_bits_to_f32(p.bias[n]) : 0.f;
+      if (e < BN) {
+        const int n = nt * BN + e;
+        rw[e] = S16 && n < p.N ? p.rw[n] : 1.f;
+        bs[e] = p.bias != nullptr && n < p.N ? bf16_bits_to_f32(p.bias[n]) : 0.f;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(col_bar);
       if (!wait_warp(col_bar, 1, p.status, abort_flag)) break;
       if (!wait_warp(&acc_full[ab], (tl >> 1) & 1, p.status, abort_flag)) break;
       tc_fence_after();
-      constexpr int kChunks = BN / 64;
+      // The columns both accumulators share are the last 64 of the first one and the
+      // first 64 of the second: held by the warps of one half, which drain them first.
+      const bool has_shared = BN == 256 && half == (ab ^ 1);
       for (int i = 0; i < kChunks; ++i) {
-        // columns shared by both accumulators first: the last 64 of the first one, the first 64 of the second
-        const int c0 = ((BN == 256 && ab == 0 ? kChunks - 1 : 0) + i) % kChunks * 64;
+        const int c0 = half * kCols + (BN == 256 && ab == 0 && half == 1 ? kChunks - 1 - i : i) * 64;
         float v[64];
         tmem_ld64(tmem + ab * C::kAcc1 + (static_cast<uint32_t>(quad * 32) << 16) + c0, v);
-        if (BN == 256 && i == 0) release(shared_empty);
+        if (has_shared && i == 0) release(shared_empty);
         if (i == kChunks - 1) release(&acc_empty[ab]);
 #pragma unroll
         for (int q = 0; q < 64; q += 4) {
@@ -285,38 +279,36 @@ __global__ void __launch_bounds__(192, 1)
           for (int q = 0; q < 64; ++q) v[q] = gelu_sigmoid(v[q]);
         }
         const int x0 = nt * BN + c0;
-        auto store = [&](const uint8_t *src, int x) {
+        auto store = [&](int x) {
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (x < p.N && row0 < p.T) tma_store_2d(&m.out, src, x, row0);
+            if (x < p.N && row0 < p.T) tma_store_2d(&m.out, stage, x, row0);
             bulk_commit();
           }
-          buf ^= 1;
         };
-        auto buffer = [&]() {  // the store that used this buffer has read it
-          if (lane == 0) bulk_wait_read<1>();
+        auto free_buffer = [&]() {  // the warp's last store has read the buffer
+          if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
-          return stage + buf * C::kOutBytes;
         };
         if (p.out_f32) {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            uint8_t *dst = buffer();
+            free_buffer();
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<float4 *>(dst + sw128_offset(lane, q)) = make_float4(
+              *reinterpret_cast<float4 *>(stage + sw128_offset(lane, q)) = make_float4(
                   v[32 * hf + 4 * q], v[32 * hf + 4 * q + 1], v[32 * hf + 4 * q + 2], v[32 * hf + 4 * q + 3]);
-            store(dst, x0 + 32 * hf);
+            store(x0 + 32 * hf);
           }
         } else {
-          uint8_t *dst = buffer();
+          free_buffer();
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<uint4 *>(dst + sw128_offset(lane, q)) =
+            *reinterpret_cast<uint4 *>(stage + sw128_offset(lane, q)) =
                 make_uint4(cvt_bf16x2(v[8 * q], v[8 * q + 1]), cvt_bf16x2(v[8 * q + 2], v[8 * q + 3]),
                            cvt_bf16x2(v[8 * q + 4], v[8 * q + 5]), cvt_bf16x2(v[8 * q + 6], v[8 * q + 7]));
-          store(dst, x0);
+          store(x0);
         }
       }
     }
@@ -349,7 +341,7 @@ cudaError_t launch_form(const LinearFp4Params &p, LinearFp4Maps m, int sms, cuda
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(192);
+  cfg.blockDim = dim3(320);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -364,11 +356,14 @@ cudaError_t launch_linear_fp4(const LinearFp4Params &p, const LinearFp4Maps &m, 
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // waves of the pair form and of the single form, whose wave takes about half as long
-  const int64_t pair = static_cast<int64_t>((p.T + 255) / 256) * ((p.N + 255) / 256);
-  const int64_t single = static_cast<int64_t>((p.T + 127) / 128) * ((p.N + 127) / 128);
-  const int64_t pair_waves = (pair + sms / 2 - 1) / (sms / 2), single_waves = (single + sms - 1) / sms;
-  return 2 * pair_waves <= single_waves ? launch_form<2, 256>(p, m, sms, s) : launch_form<1, 128>(p, m, sms, s);
+  return m.pair ? launch_form<2, 256>(p, m, sms, s) : launch_form<1, 128>(p, m, sms, s);
+}
+
+// The form whose waves over 148 SMs are fewer: a wave of pair tiles takes about as
+// long as one of single tiles.
+bool linear_fp4_pair(int64_t T, int64_t N) {
+  const int64_t pair = ((T + 255) / 256) * ((N + 255) / 256), single = ((T + 127) / 128) * ((N + 127) / 128);
+  return (pair + 73) / 74 < (single + 147) / 148;
 }
 
 }  // namespace cm

@@ -315,13 +315,48 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// This CTA's part of a pair's tile: the bytes land here, the count on the mbarrier at
-// `bar` (a cluster address, of either CTA).
-__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *tm, uint32_t bar, int x, int y) {
+// Loads whose bytes land in this CTA and are counted on the mbarrier at `bar`, a
+// cluster address: with CG = 2 that of either CTA of the pair, else its own. Issued by the
+// lane whose `lead` is not 0.
+template <int CG>
+__device__ __forceinline__ void tma_load_2d_lead(void *dst, const CUtensorMap *tm, uint32_t bar, int x, int y,
+                                                 uint32_t lead) {
+#define CM_TMA_2D(GROUP)                                                                                        \
+  asm volatile(                                                                                                 \
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"                                                         \
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes" GROUP                \
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(smem_u32(dst)),                                                 \
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y), "r"(lead)                                  \
+      : "memory")
+  if (CG == 2)
+    CM_TMA_2D(".cta_group::2");
+  else
+    CM_TMA_2D("");
+#undef CM_TMA_2D
+}
+
+template <int CG>
+__device__ __forceinline__ void tma_load_3d_lead(void *dst, const CUtensorMap *tm, uint32_t bar, int x, int y, int z,
+                                                 uint32_t lead) {
+#define CM_TMA_3D(GROUP)                                                                                        \
+  asm volatile(                                                                                                 \
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"                                                         \
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes" GROUP                \
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(smem_u32(dst)),                                             \
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(lead)                          \
+      : "memory")
+  if (CG == 2)
+    CM_TMA_3D(".cta_group::2");
+  else
+    CM_TMA_3D("");
+#undef CM_TMA_3D
+}
+
+__device__ __forceinline__ void mbar_arrive_expect_tx_lead(uint64_t *bar, uint32_t bytes, uint32_t lead) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, "
-      "%4}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y)
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(bytes), "r"(lead)
       : "memory");
 }
 
@@ -336,13 +371,23 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// Arrives on both CTAs' copies of `bar` once the pair's tcgen05 operations issued so far by this thread are complete.
-__device__ __forceinline__ void umma_commit_pair(uint64_t *bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
+// Arrives on `bar` (CG = 2: on both CTAs' copies) once the tcgen05 operations issued so far by the lane
+// whose `lead` is not 0 are complete.
+template <int CG>
+__device__ __forceinline__ void umma_commit_lead(uint64_t *bar, uint32_t lead) {
+  if (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3)), "r"(lead)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
