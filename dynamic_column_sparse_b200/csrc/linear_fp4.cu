@@ -38,8 +38,8 @@ struct LinCfg {
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
   static constexpr uint32_t kOutBytes = 4096;  // 32 rows x 128 bytes, one per epilogue warp
   static constexpr uint32_t kOutOff = kStages * kStageBytes;
-  static constexpr uint32_t kColOff = kOutOff + 8 * kOutBytes;  // [2][BN] fp32: row scales of w, bias
-  static constexpr uint32_t kBarOff = kColOff + 2 * BN * 4;
+  static constexpr uint32_t kColOff = kOutOff + 8 * kOutBytes;  // [BN] row scale of w and bias, bf16 each
+  static constexpr uint32_t kBarOff = kColOff + BN * 4;
   static constexpr uint32_t kSmem = 1024 + kBarOff + 256;
   static constexpr uint32_t kAcc1 = BN == 256 ? 192 : BN;        // TMEM column of the second accumulator
   static constexpr uint32_t kSfCol = kAcc1 + BN;                 // scale slots: 4 columns of x, BN / 32 of w
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(320, 1)
     const int half = (warp - 2) >> 2;
     const int e = threadIdx.x - 64;
     uint8_t *stage = smem + C::kOutOff + (warp - 2) * C::kOutBytes;
-    float *rw = reinterpret_cast<float *>(smem + C::kColOff), *bs = rw + BN;
+    uint32_t *cols = reinterpret_cast<uint32_t *>(smem + C::kColOff);
     int tl = 0;
     // a drained accumulator (or its shared columns) goes back to the leader's MMA warp
     auto release = [&](uint64_t *bar) {
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(320, 1)
       __syncwarp();
       if (lane == 0) {
         if (CG == 2)
-          mbar_arrive_cluster(cluster_addr(bar, 0));
+          mbar_arrive_cluster_relaxed(cluster_addr(bar, 0));
         else
           mbar_arrive(bar);
       }
@@ -242,15 +242,18 @@ __global__ void __launch_bounds__(320, 1)
       const int mt = tile / tiles_n, nt = tile - mt * tiles_n;
       const int ab = tl & 1;
       const int row0 = (mt * CG + rank) * 128 + quad * 32;
+      // this row's factor; this thread's column: row scale of w above, bias below, both bf16
       const float rx = S16 && row0 + lane < p.T ? p.rx[row0 + lane] : 1.f;
+      const int n = nt * BN + e;
+      uint32_t col = 0x3f800000u;
+      if (e < BN && n < p.N) {
+        if (S16) col = static_cast<uint32_t>(f32_to_bf16_bits(p.rw[n])) << 16;
+        if (p.bias != nullptr) col |= p.bias[n];
+      }
       // the warps have read the previous tile's column values; put this tile's in place
       if (lane == 0) mbar_arrive(col_bar);
       if (!wait_warp(col_bar, 0, p.status, abort_flag)) break;
-      if (e < BN) {
-        const int n = nt * BN + e;
-        rw[e] = S16 && n < p.N ? p.rw[n] : 1.f;
-        bs[e] = p.bias != nullptr && n < p.N ? bf16_bits_to_f32(p.bias[n]) : 0.f;
-      }
+      if (e < BN) cols[e] = col;
       __syncwarp();
       if (lane == 0) mbar_arrive(col_bar);
       if (!wait_warp(col_bar, 1, p.status, abort_flag)) break;
@@ -265,14 +268,21 @@ __global__ void __launch_bounds__(320, 1)
         tmem_ld64(tmem + ab * C::kAcc1 + (static_cast<uint32_t>(quad * 32) << 16) + c0, v);
         if (has_shared && i == 0) release(shared_empty);
         if (i == kChunks - 1) release(&acc_empty[ab]);
+        // Every lane reads every column's values, a shared-memory wavefront for each
+        // word: with fp32 values these reads were the longest part of the epilogue.
 #pragma unroll
-        for (int q = 0; q < 64; q += 4) {
-          const float4 f = *reinterpret_cast<const float4 *>(rw + c0 + q);
-          const float4 g = *reinterpret_cast<const float4 *>(bs + c0 + q);
-          v[q] = fmaf(v[q], rx * f.x, g.x);
-          v[q + 1] = fmaf(v[q + 1], rx * f.y, g.y);
-          v[q + 2] = fmaf(v[q + 2], rx * f.z, g.z);
-          v[q + 3] = fmaf(v[q + 3], rx * f.w, g.w);
+        for (int g = 0; g < 64; g += 16) {
+          uint4 w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const uint4 *>(cols + c0 + g + 4 * q);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint32_t w0 = q & 1 ? w[q >> 1].z : w[q >> 1].x, w1 = q & 1 ? w[q >> 1].w : w[q >> 1].y;
+            float2 &u = *reinterpret_cast<float2 *>(v + g + 2 * q);
+            const float2 o = make_float2(bf16_lo(w0), bf16_lo(w1));
+            u = S16 ? fma2(u, mul2(make_float2(rx, rx), make_float2(bf16_hi(w0), bf16_hi(w1))), o)
+                    : make_float2(u.x + o.x, u.y + o.y);
+          }
         }
         if (p.gelu) {
 #pragma unroll

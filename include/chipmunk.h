@@ -390,7 +390,9 @@ CHIPMUNK_API chipmunk_status chipmunk_scatter_cols(const void *packed, int64_t n
  *               tiles of 128 rows consecutive along the columns, padded to whole
  *               256 columns (padding blocks of a row hold 0; bytes of rows past
  *               the last are not written)
- *   row_scales  [rows] fp32 (NVFP4; not used and may be NULL for MXFP4)
+ *   row_scales  [rows] fp32 (NVFP4; not used and may be NULL for MXFP4): powers of
+ *               two or NaN (chipmunk_linear_fp4 takes w's rounded to bf16, which
+ *               changes none of those)
  */
 #define CHIPMUNK_NVFP4 0
 #define CHIPMUNK_MXFP4 1
