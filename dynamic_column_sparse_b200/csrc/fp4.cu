@@ -1,10 +1,10 @@
 // fp4.cu - rows of bf16 values to 4-bit microscaled codes (the operands of the
 // block-scaled product) and back. Formats and scale layout: fp4.cuh.
 //
-// Quantiser: one warp per row, 16 columns (two 16-byte loads, one 8-byte store)
-// per lane and step; the block maxima come from packed 16-bit maxima of the
-// bits. NVFP4 needs the row's maximum before its first code and reads the row
-// twice, the second time from cache.
+// Both are HBM bound. Quantiser: a row is read once and held in registers as bf16 by
+// one warp (up to 4096 columns) or by 4 or 16 warps of a CTA, 16 consecutive columns per
+// lane and step, so that NVFP4's row maximum costs no second pass; the block maxima
+// come from packed 16-bit maxima of the bits, and no value is divided (e2m1_grid).
 #include <algorithm>
 
 #include "fp4.cuh"
@@ -13,64 +13,84 @@
 namespace cm {
 namespace {
 
-template <int FMT>
-__global__ void __launch_bounds__(256) quantize_fp4_rows_kernel(const Fp4QuantParams p) {
+// W warps per row, NV steps of 16 columns per lane.
+template <int FMT, int W, int NV>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) quantize_fp4_rows_kernel(const Fp4QuantParams p) {
+  constexpr int G = 32 * W, kRows = W == 1 ? 4 : 1;
+  constexpr int kLanes = FMT == kNvfp4 ? 1 : 2;  // lanes per block
+  __shared__ uint32_t row_max[2][16];
   if (*(volatile const int *)p.status != kDevOk) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  const int t = threadIdx.x % G, lane = threadIdx.x & 31;
   const int groups = static_cast<int>(p.cols / 16);
+  const int pad_groups = (groups + 15) / 16 * 16;  // whole 256 columns carry scale bytes
   const int64_t tiles = fp4_scale_tiles(p.cols, FMT);
-  // groups that carry scale bytes: whole 256-column tiles, the padding written as zero scales
-  const int pad_groups = static_cast<int>((p.cols + 255) / 256 * 16);
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); row < p.rows;
-       row += warps) {
-    const uint4 *src = reinterpret_cast<const uint4 *>(p.x + row * p.cols);
+  const bool wide = (reinterpret_cast<uintptr_t>(p.x) & 31) == 0;
+  int slot = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G; row < p.rows;
+       row += static_cast<int64_t>(gridDim.x) * kRows) {
+    const uint16_t *src = p.x + row * p.cols;
+    Vec32 u[NV];
+    if (wide) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) u[v] = v * G + t < groups ? load32(src + 16 * (v * G + t)) : Vec32{};
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) u[v] = v * G + t < groups ? load16x2(src + 16 * (v * G + t)) : Vec32{};
+    }
+    uint32_t m[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a = amax_bf16x2(a, u[v].w[e]);
+      m[v] = amax_fold(a);
+    }
     float rs_inv = 1.f;
     if (FMT == kNvfp4) {
-      uint32_t m = 0;
-      for (int g = lane; g < groups; g += 32) {
-        const uint4 u[2] = {src[2 * g], src[2 * g + 1]};
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(u);
+      uint32_t amax = m[0];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = amax_bf16x2(m, w[e]);
+      for (int v = 1; v < NV; ++v) amax = max(amax, m[v]);
+      amax = __reduce_max_sync(0xffffffffu, amax);
+      if (W > 1) {
+        if (lane == 0) row_max[slot][t >> 5] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) amax = max(amax, row_max[slot][w]);
+        slot ^= 1;
       }
-      const uint32_t amax = __reduce_max_sync(0xffffffffu, amax_fold(m));
       const float rs = nvfp4_row_scale(amax);
       rs_inv = amax >= kBf16Inf ? 0.f : __frcp_rn(rs);
-      if (lane == 0) p.row_scales[row] = rs;
+      if (t == 0) p.row_scales[row] = rs;
     }
     uint2 *dst = reinterpret_cast<uint2 *>(p.codes + row * (p.cols / 2));
-    for (int g0 = 0; g0 < pad_groups; g0 += 32) {
-      const int g = g0 + lane;
-      const bool live = g < groups;
-      uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-      if (live) {
-        u[0] = src[2 * g];
-        u[1] = src[2 * g + 1];
-      }
-      const uint32_t *w = reinterpret_cast<const uint32_t *>(u);
-      uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = amax_bf16x2(m, w[e]);
-      uint32_t amax = amax_fold(m);
+    for (int v = 0; v < NV; ++v) {
+      const int g = v * G + t;
       float inv;
       uint32_t sb;
       if (FMT == kNvfp4) {
-        sb = nvfp4_block_scale(amax, rs_inv, &inv);
+        sb = nvfp4_block_scale(m[v], rs_inv, &inv);
       } else {
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        sb = mxfp4_block_scale(amax, &inv);
+        sb = mxfp4_block_scale(max(m[v], __shfl_xor_sync(0xffffffffu, m[v], 1)), &inv);
       }
-      if (!live) sb = 0;
-      float v[16];
+      if (g < groups) {
+        float q[16];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[2 * e] = FMT == kNvfp4 ? e2m1_grid(bf16_lo(w[e]), inv) : bf16_lo(w[e]) * inv;
-        v[2 * e + 1] = FMT == kNvfp4 ? e2m1_grid(bf16_hi(w[e]), inv) : bf16_hi(w[e]) * inv;
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t w = u[v].w[e];
+          if (FMT == kNvfp4) {
+            const float2 c = make_float2(0x1.8p11f, 0x1.8p11f), n = make_float2(-0x1.8p11f, -0x1.8p11f);
+            const float2 d = add2(fma2(make_float2(bf16_lo(w), bf16_hi(w)), make_float2(inv, inv), c), n);
+            q[2 * e] = d.x, q[2 * e + 1] = d.y;
+          } else {
+            q[2 * e] = bf16_lo(w) * inv, q[2 * e + 1] = bf16_hi(w) * inv;
+          }
+        }
+        dst[g] = make_uint2(e2m1x8(q), e2m1x8(q + 8));
+      } else {
+        sb = 0;
       }
-      if (live) dst[g] = make_uint2(e2m1x8(v), e2m1x8(v + 8));
       // four blocks' scale bytes to one word, written by the first lane of each four blocks
-      constexpr int kLanes = FMT == kNvfp4 ? 1 : 2;  // lanes per block
       uint32_t word = sb;
 #pragma unroll
       for (int i = 1; i < 4; ++i) word |= __shfl_down_sync(0xffffffffu, sb, i * kLanes) << (8 * i);
@@ -80,69 +100,103 @@ __global__ void __launch_bounds__(256) quantize_fp4_rows_kernel(const Fp4QuantPa
   }
 }
 
-// 16 columns per thread: one 8-byte code load, one scale byte, two (bf16) or
-// four (fp32) 16-byte stores. Every value (two code bits times four scale bits
-// times powers of two) is exact in bf16 within its range.
+// Four e2m1 codes (16 bits) to four bf16: the high and low bytes of the magnitudes
+// 0, 0.5 .. 6 by byte permutes with the codes as selectors, then the signs.
+__device__ __forceinline__ uint2 e2m1x4_to_bf16(uint32_t c) {
+  const uint32_t sel = c & 0x7777u;
+  const uint32_t hi = __byte_perm(0x3f3f3f00u, 0x40404040u, sel);  // 00 3f 3f 3f | 40 40 40 40
+  const uint32_t lo = __byte_perm(0xc0800000u, 0xc0804000u, sel);  // 00 00 80 c0 | 00 40 80 c0
+  const uint32_t a = __byte_perm(lo, hi, 0x5140u), b = __byte_perm(lo, hi, 0x7362u);
+  return make_uint2(a | (c & 8u) << 12 | (c & 0x80u) << 24, b | (c & 0x800u) << 4 | (c & 0x8000u) << 16);
+}
+
+// A thread takes 16 columns of a row: one 8-byte code load, one scale byte, one
+// 32-byte (bf16) or two (fp32) stores. Every value (two code bits times four scale bits times
+// powers of two) is exact in bf16 within its range, and so is the product taken in fp32.
 template <int FMT, bool F32>
 __global__ void __launch_bounds__(256) dequantize_fp4_rows_kernel(const Fp4QuantParams p, void *out) {
   if (*(volatile const int *)p.status != kDevOk) return;
   const int groups = static_cast<int>(p.cols / 16);
   const int64_t tiles = fp4_scale_tiles(p.cols, FMT);
-  const int64_t total = p.rows * groups;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t row = i / groups;
-    const int g = static_cast<int>(i - row * groups);
+  const int g = blockIdx.x * 32 + threadIdx.x;
+  if (g >= groups) return;
+  const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.y) * 8 + threadIdx.y; row < p.rows;
+       row += static_cast<int64_t>(gridDim.y) * 8) {
+    const int64_t i = row * groups + g;
     const uint2 c = reinterpret_cast<const uint2 *>(p.codes)[i];
     const uint32_t sb = p.scales[fp4_scale_offset(row, FMT == kNvfp4 ? g : g / 2, tiles)];
     const float s = FMT == kNvfp4 ? e4m3_to_f32(sb) * p.row_scales[row] : e8m0_to_f32(sb);
-    float v[16];
+    const uint2 h[4] = {e2m1x4_to_bf16(c.x & 0xffffu), e2m1x4_to_bf16(c.x >> 16), e2m1x4_to_bf16(c.y & 0xffffu),
+                        e2m1x4_to_bf16(c.y >> 16)};
+    float2 v[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const uint32_t code = ((e < 8 ? c.x : c.y) >> (4 * (e & 7))) & 15u;
-      // magnitudes 0, 0.5, then (2 + low bit) * 2^(exponent - 2)
-      const uint32_t mag = code & 7u;
-      const float a = mag < 2 ? 0.5f * static_cast<float>(mag)
-                              : __uint_as_float(((mag >> 1) + 126u) << 23 | (mag & 1u) << 22);
-      v[e] = (code & 8u ? -a : a) * s;
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t w = e & 1 ? h[e >> 1].y : h[e >> 1].x;
+      v[e] = mul2(make_float2(bf16_lo(w), bf16_hi(w)), make_float2(s, s));
     }
     if (F32) {
-      float4 *o = reinterpret_cast<float4 *>(out) + i * 4;
+      uint4 *o = reinterpret_cast<uint4 *>(out) + i * 4;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) o[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      for (int q = 0; q < 4; ++q)
+        o[q] = make_uint4(__float_as_uint(v[2 * q].x), __float_as_uint(v[2 * q].y), __float_as_uint(v[2 * q + 1].x),
+                          __float_as_uint(v[2 * q + 1].y));
     } else {
-      uint4 *o = reinterpret_cast<uint4 *>(out) + i * 2;
+      uint32_t w[8];
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        o[q] = make_uint4(cvt_bf16x2(v[8 * q], v[8 * q + 1]), cvt_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                          cvt_bf16x2(v[8 * q + 4], v[8 * q + 5]), cvt_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+      for (int e = 0; e < 8; ++e) w[e] = cvt_bf16x2(v[e].x, v[e].y);
+      uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + i * 16);
+      if (wide) {
+        store32(o, w);
+      } else {
+        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
     }
   }
 }
 
 }  // namespace
 
+namespace {
+
+template <int FMT, int W>
+void launch_w(const Fp4QuantParams &p, cudaStream_t s) {
+  const int need = static_cast<int>((p.cols / 16 + 32 * W - 1) / (32 * W));
+  const int rows = W == 1 ? 4 : 1;
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((p.rows + rows - 1) / rows, 148 * (W == 16 ? 4 : 16)));
+  const unsigned threads = W == 1 ? 128 : 32 * W;
+  if (need <= 1) quantize_fp4_rows_kernel<FMT, W, 1><<<blocks, threads, 0, s>>>(p);
+  else if (need <= 2) quantize_fp4_rows_kernel<FMT, W, 2><<<blocks, threads, 0, s>>>(p);
+  else if (need <= 4) quantize_fp4_rows_kernel<FMT, W, 4><<<blocks, threads, 0, s>>>(p);
+  else if (need <= 6) quantize_fp4_rows_kernel<FMT, W, 6><<<blocks, threads, 0, s>>>(p);
+  else quantize_fp4_rows_kernel<FMT, W, 8><<<blocks, threads, 0, s>>>(p);
+}
+
+template <int FMT>
+void launch_fmt(const Fp4QuantParams &p, cudaStream_t s) {
+  if (p.cols <= 4096) launch_w<FMT, 1>(p, s);
+  else if (p.cols <= 16384) launch_w<FMT, 4>(p, s);
+  else launch_w<FMT, 16>(p, s);
+}
+
+}  // namespace
+
 cudaError_t launch_quantize_fp4_rows(const Fp4QuantParams &p, cudaStream_t s) {
   if (p.rows <= 0) return cudaSuccess;
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((p.rows + 7) / 8, 148 * 8));
-  if (p.fmt == kNvfp4)
-    quantize_fp4_rows_kernel<kNvfp4><<<blocks, 256, 0, s>>>(p);
-  else
-    quantize_fp4_rows_kernel<kMxfp4><<<blocks, 256, 0, s>>>(p);
+  if (p.fmt == kNvfp4) launch_fmt<kNvfp4>(p, s);
+  else launch_fmt<kMxfp4>(p, s);
   return cudaGetLastError();
 }
 
 cudaError_t launch_dequantize_fp4_rows(const Fp4QuantParams &p, bool f32, void *out, cudaStream_t s) {
   if (p.rows <= 0) return cudaSuccess;
-  const int64_t total = p.rows * (p.cols / 16);
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((total + 255) / 256, 148 * 32));
-  if (p.fmt == kNvfp4) {
-    if (f32) dequantize_fp4_rows_kernel<kNvfp4, true><<<blocks, 256, 0, s>>>(p, out);
-    else dequantize_fp4_rows_kernel<kNvfp4, false><<<blocks, 256, 0, s>>>(p, out);
-  } else {
-    if (f32) dequantize_fp4_rows_kernel<kMxfp4, true><<<blocks, 256, 0, s>>>(p, out);
-    else dequantize_fp4_rows_kernel<kMxfp4, false><<<blocks, 256, 0, s>>>(p, out);
-  }
+  const unsigned x = static_cast<unsigned>((p.cols / 16 + 31) / 32);
+  const int64_t y = std::min<int64_t>((p.rows + 7) / 8, std::max<int64_t>(1, 148 * 64 / x));
+  const dim3 grid(x, static_cast<unsigned>(y)), block(32, 8);
+  auto kernel = p.fmt == kNvfp4 ? (f32 ? dequantize_fp4_rows_kernel<kNvfp4, true> : dequantize_fp4_rows_kernel<kNvfp4, false>)
+                                : (f32 ? dequantize_fp4_rows_kernel<kMxfp4, true> : dequantize_fp4_rows_kernel<kMxfp4, false>);
+  kernel<<<grid, block, 0, s>>>(p, out);
   return cudaGetLastError();
 }
 

@@ -14,7 +14,7 @@
 // partial sums of a row's warps joined through shared memory by the pairwise
 // rule for means and squares, so no large mean cancels.
 //
-// A row is held by one warp (up to 1024 columns) or by 4, 8 or 16 warps of one
+// A row is held by one warp (up to 1024 columns) or by 4 or 16 warps of one
 // CTA, NV groups of 8 columns per thread; column group v * G + t belongs to
 // thread t, so every access is 16 bytes per lane and consecutive over a warp.
 #include <algorithm>
@@ -25,17 +25,38 @@
 namespace cm {
 namespace {
 
-__device__ __forceinline__ void load8(const void *p, int f32, int64_t i, float *v) {
-  if (f32) {
-    const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    const float4 a = s[0], b = s[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// Eight columns as they lie in memory, bf16 or fp32.
+template <bool F32>
+struct Raw8 {
+  uint4 w[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> raw8(const void *p, int64_t i) {
+  Raw8<F32> r;
+  const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) + i * (F32 ? 4 : 2));
+  r.w[0] = s[0];
+  if (F32) r.w[F32 ? 1 : 0] = s[1];
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void unpack8(const Raw8<F32> &r, float *v) {
+  if (F32) {
+    const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[F32].x, r.w[F32].y, r.w[F32].z, r.w[F32].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
   } else {
-    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(w[e]), v[2 * e + 1] = bf16_hi(w[e]);
   }
+}
+
+// Eight values of a vector shared by many rows (weights, gates, scales, shifts), bf16 or fp32.
+__device__ __forceinline__ void load8(const void *p, int f32, int64_t i, float *v) {
+  if (f32)
+    unpack8<true>(raw8<true>(p, i), v);
+  else
+    unpack8<false>(raw8<false>(p, i), v);
 }
 
 __device__ __forceinline__ uint4 pack8(const float *v) {
@@ -64,7 +85,7 @@ struct RowStats {
     int n8 = 0;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-      if (v < nv) {
+      if (v < NV - 1 || v < nv) {
         ++n8;
         if (layer) {
 #pragma unroll
@@ -79,7 +100,7 @@ struct RowStats {
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-      if (v < nv) {
+      if (v < NV - 1 || v < nv) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float d = r[v][e] - mean;
@@ -142,7 +163,7 @@ __device__ __forceinline__ int sample_of(const int32_t *off, int B, int64_t t) {
   return lo;
 }
 
-template <int W, int NV>
+template <int W, int NV, bool R32, bool Y32>
 __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(const NormParams p) {
   constexpr int G = 32 * W;                   // threads per row
   constexpr int kRows = (W == 1 ? 128 : G) / G;  // rows a CTA works on at a time
@@ -152,26 +173,47 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
   const int D = p.D, ng = D / 8;
   const int nv = t < ng ? (ng - 1 - t) / G + 1 : 0;  // column groups of this thread
   RowStats<W> st{buf};
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G; row < p.T;
-       row += static_cast<int64_t>(gridDim.x) * kRows) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  // The next row's loads are issued before the current row's arithmetic: registers hold one
+  // row of inputs in flight per thread.
+  Raw8<R32> res[NV];
+  Raw8<Y32> y[NV];
+  auto fetch = [&](int64_t row) {
+    if (row >= p.T) return;
+    const int64_t base = row * D;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (v < NV - 1 || v < nv) {  // only a thread's last group may be missing
+        res[v] = raw8<R32>(p.res, base + (v * G + t) * 8);
+        if (p.y != nullptr) y[v] = raw8<Y32>(p.y, base + (v * G + t) * 8);
+      }
+    }
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G;
+  fetch(row);
+  for (; row < p.T; row += step) {
+    float r[NV][8], a0[NV][8];
+    const bool has_y = p.y != nullptr;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (has_y) unpack8<Y32>(y[v], r[v]);
+      unpack8<R32>(res[v], a0[v]);
+    }
+    fetch(row + step);
     int b = 0;
     if (p.offsets != nullptr) {
-      b = sample_of(p.offsets, static_cast<int>(p.B), row);
+      b = sample_of(p.offsets, p.B, row);
       if (b < 0) continue;  // the same for all threads of the row
     }
     const int64_t mod = static_cast<int64_t>(b) * p.ld_mod;
     const int64_t base = row * D;
-    float r[NV][8];
-    if (p.y != nullptr) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (v < nv) load8(p.y, p.y_f32, base + (v * G + t) * 8, r[v]);
+    if (has_y) {
       float2 ms = make_float2(0.f, 1.f);
       if (p.post_norm != kNormNone)
         ms = st.template norm<NV>(r, nv, warp, lane, G, D, p.post_norm == kNormLayer, p.eps);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        if (v < nv) {
+        if (v < NV - 1 || v < nv) {
           const int c = (v * G + t) * 8;
           float a[8];
           if (p.post_norm != kNormNone) {
@@ -188,25 +230,21 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
 #pragma unroll
             for (int e = 0; e < 8; ++e) r[v][e] *= a[e];
           }
-          load8(p.res, p.res_f32, base + c, a);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r[v][e] = fmaf(p.res_scale, a[e], r[v][e]);
+          for (int e = 0; e < 8; ++e) r[v][e] = fmaf(p.res_scale, a0[v][e], r[v][e]);
         }
     } else {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        if (v < nv) {
-          load8(p.res, p.res_f32, base + (v * G + t) * 8, r[v]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r[v][e] *= p.res_scale;
-        }
+        for (int e = 0; e < 8; ++e) r[v][e] = p.res_scale * a0[v][e];
     }
     if (p.res_out != nullptr) {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        if (v < nv) {
+        if (v < NV - 1 || v < nv) {
           const int64_t i = base + (v * G + t) * 8;
-          if (p.res_f32) {
+          if (R32) {
             float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.res_out) + i);
             o[0] = make_float4(r[v][0], r[v][1], r[v][2], r[v][3]);
             o[1] = make_float4(r[v][4], r[v][5], r[v][6], r[v][7]);
@@ -221,7 +259,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       h[v] = make_uint4(0, 0, 0, 0);
-      if (v < nv) {
+      if (v < NV - 1 || v < nv) {
         const int c = (v * G + t) * 8;
         float a[8];
 #pragma unroll
@@ -252,7 +290,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
     if (p.out_format == kOutBf16) {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        if (v < nv)
+        if (v < NV - 1 || v < nv)
           *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + base + (v * G + t) * 8) = h[v];
       continue;
     }
@@ -271,7 +309,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
       if (t == 0) p.out_row_scales[row] = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        if (v < nv) {
+        if (v < NV - 1 || v < nv) {
           const uint32_t w[4] = {h[v].x, h[v].y, h[v].z, h[v].w};
           uint32_t o[2] = {0, 0};
 #pragma unroll
@@ -327,17 +365,29 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
   }
 }
 
+template <int W, int NV>
+void launch_nv(const NormParams &p, unsigned blocks, cudaStream_t s) {
+  const unsigned threads = W == 1 ? 128 : 32 * W;
+  if (p.res_f32) {
+    if (p.y_f32) norm_residual_kernel<W, NV, true, true><<<blocks, threads, 0, s>>>(p);
+    else norm_residual_kernel<W, NV, true, false><<<blocks, threads, 0, s>>>(p);
+  } else {
+    if (p.y_f32) norm_residual_kernel<W, NV, false, true><<<blocks, threads, 0, s>>>(p);
+    else norm_residual_kernel<W, NV, false, false><<<blocks, threads, 0, s>>>(p);
+  }
+}
+
 template <int W>
 cudaError_t launch_w(const NormParams &p, cudaStream_t s) {
   const int need = (p.D / 8 + 32 * W - 1) / (32 * W);
   const int rows = W == 1 ? 4 : 1;
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((p.T + rows - 1) / rows, 148 * 16));
-  const unsigned threads = W == 1 ? 128 : 32 * W;
+  // resident CTAs, so that each prefetches its next row (W = 16: one or two per SM)
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((p.T + rows - 1) / rows, 148 * (W == 16 ? 2 : 6)));
   switch (need) {
-    case 1: norm_residual_kernel<W, 1><<<blocks, threads, 0, s>>>(p); break;
-    case 2: norm_residual_kernel<W, 2><<<blocks, threads, 0, s>>>(p); break;
-    case 3: norm_residual_kernel<W, 3><<<blocks, threads, 0, s>>>(p); break;
-    default: norm_residual_kernel<W, 4><<<blocks, threads, 0, s>>>(p); break;
+    case 1: launch_nv<W, 1>(p, blocks, s); break;
+    case 2: launch_nv<W, 2>(p, blocks, s); break;
+    case 3: launch_nv<W, 3>(p, blocks, s); break;
+    default: launch_nv<W, 4>(p, blocks, s); break;
   }
   return cudaGetLastError();
 }
@@ -348,7 +398,6 @@ cudaError_t launch_norm_residual(const NormParams &p, cudaStream_t s) {
   if (p.T <= 0) return cudaSuccess;
   if (p.D <= 32 * 8 * 4) return launch_w<1>(p, s);
   if (p.D <= 128 * 8 * 4) return launch_w<4>(p, s);
-  if (p.D <= 256 * 8 * 4) return launch_w<8>(p, s);
   return launch_w<16>(p, s);
 }
 
