@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) quantize_fp4_rows_kerne
         slot ^= 1;
       }
       const float rs = nvfp4_row_scale(amax);
-      rs_inv = amax >= kBf16Inf ? 0.f : __frcp_rn(rs);
+      rs_inv = nvfp4_row_inv(amax);
       if (t == 0) p.row_scales[row] = rs;
     }
     uint2 *dst = reinterpret_cast<uint2 *>(p.codes + row * (p.cols / 2));
@@ -78,24 +78,17 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) quantize_fp4_rows_kerne
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const uint32_t w = u[v].w[e];
-          if (FMT == kNvfp4) {
-            const float2 c = make_float2(0x1.8p11f, 0x1.8p11f), n = make_float2(-0x1.8p11f, -0x1.8p11f);
-            const float2 d = add2(fma2(make_float2(bf16_lo(w), bf16_hi(w)), make_float2(inv, inv), c), n);
-            q[2 * e] = d.x, q[2 * e + 1] = d.y;
-          } else {
-            q[2 * e] = bf16_lo(w) * inv, q[2 * e + 1] = bf16_hi(w) * inv;
-          }
+          const float2 x = make_float2(bf16_lo(w), bf16_hi(w));
+          const float2 d = FMT == kNvfp4 ? e2m1_grid(x, inv) : mul2(x, make_float2(inv, inv));
+          q[2 * e] = d.x, q[2 * e + 1] = d.y;
         }
         dst[g] = make_uint2(e2m1x8(q), e2m1x8(q + 8));
       } else {
         sb = 0;
       }
-      // four blocks' scale bytes to one word, written by the first lane of each four blocks
-      uint32_t word = sb;
-#pragma unroll
-      for (int i = 1; i < 4; ++i) word |= __shfl_down_sync(0xffffffffu, sb, i * kLanes) << (8 * i);
-      if ((lane & (4 * kLanes - 1)) == 0 && g < pad_groups)
-        *reinterpret_cast<uint32_t *>(p.scales + fp4_scale_offset(row, g / kLanes, tiles)) = word;
+      // one byte per block; a warp's stores to the same four blocks merge into one word
+      if ((lane & (kLanes - 1)) == 0 && g < pad_groups)
+        p.scales[fp4_scale_offset(row, g / kLanes, tiles)] = static_cast<uint8_t>(sb);
     }
   }
 }
@@ -110,47 +103,57 @@ __device__ __forceinline__ uint2 e2m1x4_to_bf16(uint32_t c) {
   return make_uint2(a | (c & 8u) << 12 | (c & 0x80u) << 24, b | (c & 0x800u) << 4 | (c & 0x8000u) << 16);
 }
 
-// A thread takes 16 columns of a row: one 8-byte code load, one scale byte, one
-// 32-byte (bf16) or two (fp32) stores. Every value (two code bits times four scale bits times
-// powers of two) is exact in bf16 within its range, and so is the product taken in fp32.
+// A thread takes 16 columns of four rows at a time: per row one 8-byte code load, one scale
+// byte, one 32-byte (bf16) or four 16-byte (fp32) stores; the rows' loads go out together.
+// Every value (two code bits times four scale bits times powers of two) and the
+// scale itself are exact in bf16 within its range, so the product is taken there.
 template <int FMT, bool F32>
 __global__ void __launch_bounds__(256) dequantize_fp4_rows_kernel(const Fp4QuantParams p, void *out) {
+  constexpr int R = 4;
   if (*(volatile const int *)p.status != kDevOk) return;
   const int groups = static_cast<int>(p.cols / 16);
   const int64_t tiles = fp4_scale_tiles(p.cols, FMT);
   const int g = blockIdx.x * 32 + threadIdx.x;
   if (g >= groups) return;
   const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.y) * 8 + threadIdx.y; row < p.rows;
-       row += static_cast<int64_t>(gridDim.y) * 8) {
-    const int64_t i = row * groups + g;
-    const uint2 c = reinterpret_cast<const uint2 *>(p.codes)[i];
-    const uint32_t sb = p.scales[fp4_scale_offset(row, FMT == kNvfp4 ? g : g / 2, tiles)];
-    const float s = FMT == kNvfp4 ? e4m3_to_f32(sb) * p.row_scales[row] : e8m0_to_f32(sb);
-    const uint2 h[4] = {e2m1x4_to_bf16(c.x & 0xffffu), e2m1x4_to_bf16(c.x >> 16), e2m1x4_to_bf16(c.y & 0xffffu),
-                        e2m1x4_to_bf16(c.y >> 16)};
-    float2 v[8];
+  const int64_t step = static_cast<int64_t>(gridDim.y) * 8;
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * 8 + threadIdx.y; row0 < p.rows; row0 += R * step) {
+    uint2 c[R];
+    uint32_t sb[R];
+    float rs[R];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t w = e & 1 ? h[e >> 1].y : h[e >> 1].x;
-      v[e] = mul2(make_float2(bf16_lo(w), bf16_hi(w)), make_float2(s, s));
+    for (int k = 0; k < R; ++k) {
+      const int64_t row = min(row0 + k * step, p.rows - 1);
+      c[k] = reinterpret_cast<const uint2 *>(p.codes)[row * groups + g];
+      sb[k] = p.scales[fp4_scale_offset(row, FMT == kNvfp4 ? g : g / 2, tiles)];
+      rs[k] = FMT == kNvfp4 ? p.row_scales[row] : 1.f;
     }
-    if (F32) {
-      uint4 *o = reinterpret_cast<uint4 *>(out) + i * 4;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        o[q] = make_uint4(__float_as_uint(v[2 * q].x), __float_as_uint(v[2 * q].y), __float_as_uint(v[2 * q + 1].x),
-                          __float_as_uint(v[2 * q + 1].y));
-    } else {
+    for (int k = 0; k < R; ++k) {
+      const int64_t row = row0 + k * step;
+      if (row >= p.rows) break;
+      const float s = FMT == kNvfp4 ? e4m3_to_f32(sb[k]) * rs[k] : e8m0_to_f32(sb[k]);
+      const uint32_t s2 = cvt_bf16x2(s, s);
+      const uint2 h[4] = {e2m1x4_to_bf16(c[k].x & 0xffffu), e2m1x4_to_bf16(c[k].x >> 16),
+                          e2m1x4_to_bf16(c[k].y & 0xffffu), e2m1x4_to_bf16(c[k].y >> 16)};
       uint32_t w[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = cvt_bf16x2(v[e].x, v[e].y);
-      uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + i * 16);
-      if (wide) {
-        store32(o, w);
+      for (int e = 0; e < 8; ++e) w[e] = F32 ? (e & 1 ? h[e >> 1].y : h[e >> 1].x) : mul_bf16x2(e & 1 ? h[e >> 1].y : h[e >> 1].x, s2);
+      const int64_t i = row * groups + g;
+      if (F32) {
+        float4 *o = reinterpret_cast<float4 *>(out) + i * 4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          o[q] = make_float4(bf16_lo(w[2 * q]) * s, bf16_hi(w[2 * q]) * s, bf16_lo(w[2 * q + 1]) * s,
+                             bf16_hi(w[2 * q + 1]) * s);
       } else {
-        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + i * 16);
+        if (wide) {
+          store32(o, w);
+        } else {
+          o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
       }
     }
   }
@@ -192,7 +195,7 @@ cudaError_t launch_quantize_fp4_rows(const Fp4QuantParams &p, cudaStream_t s) {
 cudaError_t launch_dequantize_fp4_rows(const Fp4QuantParams &p, bool f32, void *out, cudaStream_t s) {
   if (p.rows <= 0) return cudaSuccess;
   const unsigned x = static_cast<unsigned>((p.cols / 16 + 31) / 32);
-  const int64_t y = std::min<int64_t>((p.rows + 7) / 8, std::max<int64_t>(1, 148 * 64 / x));
+  const int64_t y = std::min<int64_t>((p.rows + 31) / 32, std::max<int64_t>(1, 148 * 32 / x));
   const dim3 grid(x, static_cast<unsigned>(y)), block(32, 8);
   auto kernel = p.fmt == kNvfp4 ? (f32 ? dequantize_fp4_rows_kernel<kNvfp4, true> : dequantize_fp4_rows_kernel<kNvfp4, false>)
                                 : (f32 ? dequantize_fp4_rows_kernel<kMxfp4, true> : dequantize_fp4_rows_kernel<kMxfp4, false>);

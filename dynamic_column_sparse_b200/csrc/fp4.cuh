@@ -45,14 +45,15 @@ __host__ __device__ inline size_t fp4_scale_offset(int64_t row, int64_t block, i
 }
 
 // A quotient x / (s rs) of a bf16 x by an e4m3 scale and a power of two lies on
-// a rounding border of e2m1 (0.25 .. 5) or at least 2^-10 away from every border,
-// while its fp32 approximation x * (1 / (s rs)) is off by at most 2^-20. Rounding
-// the product to a multiple of 2^-12 (adding and taking off 1.5 * 2^11, in the
-// fused multiply-add) therefore puts the border cases exactly on the border and
-// moves no other one across, without a division per value.
-__device__ __forceinline__ float e2m1_grid(float x, float inv) {
-  const float c = 0x1.8p11f;
-  return __fadd_rn(__fmaf_rn(x, inv, c), -c);
+// a rounding border of e2m1 (0.25 .. 5) or at least 2^-10 away from every border
+// (X 2^a - m D 2^b with integers X < 256, D < 16 and a border m is 0 or at least m / 255 of m D 2^b),
+// while its fp32 approximation x * inv, inv a reciprocal good to 2^-22, is off by less than
+// 2^-18. Rounding the product to a multiple of 2^-12 (adding and taking off 1.5 * 2^11,
+// the first in the fused multiply-add) therefore puts the border cases exactly on
+// the border and moves no other one across, without a division per value.
+__device__ __forceinline__ float2 e2m1_grid(float2 x, float inv) {
+  const float2 c = make_float2(0x1.8p11f, 0x1.8p11f), n = make_float2(-0x1.8p11f, -0x1.8p11f);
+  return add2(fma2(x, make_float2(inv, inv), c), n);
 }
 
 // Eight values to eight e2m1 codes, value i in bits 4i .. 4i+3.
@@ -110,14 +111,25 @@ __device__ __forceinline__ float nvfp4_row_scale(uint32_t amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// NVFP4 block: e4m3 scale byte and the factor that takes x to its code's grid
-// (0 for a block whose scale is 0). rs_inv = 1 / row scale (0 for a row that is
-// not finite: every scale and code is 0 and the NaN row scale speaks for it).
+// 1 / row scale (a power of two: exact), 0 for a row that is not finite, whose
+// scales and codes then are 0 while its NaN row scale speaks for it.
+__device__ __forceinline__ float nvfp4_row_inv(uint32_t amax) {
+  if (amax == 0) return 1.f;
+  if (amax >= kBf16Inf) return 0.f;
+  const int e = min(max(static_cast<int>(amax >> 7) - 127 - 10, -110), 117);
+  return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+
+// NVFP4 block: e4m3 scale byte of amax / (6 rs) and the factor that takes x to its code's
+// grid (0 for a block whose scale is 0). The quotient lies on a rounding border of e4m3 (five
+// significant bits) or at least 1 / 255 of it away; the product with 1/6 is good to 2^-23, so
+// rounding it to fp16 first (2^-12) puts the former exactly on the border and moves none across.
 __device__ __forceinline__ uint32_t nvfp4_block_scale(uint32_t amax, float rs_inv, float *inv) {
-  const float t = rs_inv != 0.f ? __fdiv_rn(__uint_as_float(amax << 16) * rs_inv, 6.f) : 0.f;
-  const __nv_fp8_storage_t b = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
-  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
-  *inv = s > 0.f ? __frcp_rn(s) * rs_inv : 0.f;
+  const float m = rs_inv != 0.f ? __uint_as_float(amax << 16) : 0.f;
+  const __half2_raw t = __half2(__float2half_rn(m * (rs_inv * (1.f / 6.f))), __half(0.f));
+  const uint32_t b = __nv_cvt_halfraw2_to_fp8x2(t, __NV_SATFINITE, __NV_E4M3) & 0xffu;
+  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3)));
+  *inv = s > 0.f ? rcp_approx(s) * rs_inv : 0.f;
   return b;
 }
 

@@ -39,29 +39,32 @@ __device__ __forceinline__ Raw8<F32> raw8(const void *p, int64_t i) {
   return r;
 }
 template <bool F32>
-__device__ __forceinline__ void unpack8(const Raw8<F32> &r, float *v) {
+__device__ __forceinline__ void unpack8(const Raw8<F32> &r, float2 *v) {
   if (F32) {
     const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[F32].x, r.w[F32].y, r.w[F32].z, r.w[F32].w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
+    for (int e = 0; e < 4; ++e) v[e] = make_float2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
   } else {
     const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(w[e]), v[2 * e + 1] = bf16_hi(w[e]);
+    for (int e = 0; e < 4; ++e) v[e] = make_float2(bf16_lo(w[e]), bf16_hi(w[e]));
   }
 }
 
 // Eight values of a vector shared by many rows (weights, gates, scales, shifts), bf16 or fp32.
-__device__ __forceinline__ void load8(const void *p, int f32, int64_t i, float *v) {
+__device__ __forceinline__ void load8(const void *p, int f32, int64_t i, float2 *v) {
   if (f32)
     unpack8<true>(raw8<true>(p, i), v);
   else
     unpack8<false>(raw8<false>(p, i), v);
 }
 
-__device__ __forceinline__ uint4 pack8(const float *v) {
-  return make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
+__device__ __forceinline__ uint4 pack8(const float2 *v) {
+  return make_uint4(cvt_bf16x2(v[0].x, v[0].y), cvt_bf16x2(v[1].x, v[1].y), cvt_bf16x2(v[2].x, v[2].y),
+                    cvt_bf16x2(v[3].x, v[3].y));
 }
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -71,74 +74,66 @@ __device__ __forceinline__ float warp_sum(float x) {
 
 // Statistics of one row over its W warps. `slot` alternates between two shared
 // buffers, so one barrier per statistic is enough.
-template <int W>
+template <int W, int NV>
 struct RowStats {
-  float2 (*buf)[16];  // [2][16]
+  float2 (*buf)[16];        // [2][16]
+  const float2 *cols;       // [W]: columns a warp holds, and 1 over that
+  float inv_d, eps;
+  int nv, warp, lane;
   int slot = 0;
 
-  // mean and 1 / sqrt(variance + eps) of the row (RMS: mean 0, mean square)
-  template <int NV>
-  __device__ __forceinline__ float2 norm(const float (&r)[NV][8], const int nv, int warp, int lane, int G, int D,
-                                         bool layer, float eps) {
-    // columns held by this warp
-    float s = 0.f, q = 0.f;
-    int n8 = 0;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-      if (v < NV - 1 || v < nv) {
-        ++n8;
-        if (layer) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s += r[v][e];
-        }
-      }
-    float mean = 0.f, n = 0.f;
+  // The row's mean and 1 / sqrt(variance + eps) (RMS: 0 and the root of the mean square), as the factor and
+  // the addend that normalise: x * factor + addend.
+  __device__ __forceinline__ float2 norm(const float2 (&r)[NV][4], bool layer) {
+    float mean = 0.f, sum = 0.f;
     if (layer) {
-      s = warp_sum(s);
-      n = 8.f * warp_sum(static_cast<float>(n8));
-      mean = n > 0.f ? s / n : 0.f;
+      float2 s = both(0.f);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (v < NV - 1 || v < nv) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s = add2(s, r[v][e]);
+        }
+      sum = warp_sum(s.x + s.y);
+      mean = sum * cols[warp].y;
     }
+    const float2 nm = both(-mean);
+    float2 q2 = both(0.f);
 #pragma unroll
     for (int v = 0; v < NV; ++v)
       if (v < NV - 1 || v < nv) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float d = r[v][e] - mean;
-          q = fmaf(d, d, q);
+        for (int e = 0; e < 4; ++e) {
+          const float2 d = add2(r[v][e], nm);
+          q2 = fma2(d, d, q2);
         }
       }
-    q = warp_sum(q);
+    float q = warp_sum(q2.x + q2.y);
     if (W > 1) {
       // join the warps: squares about the row's mean = squares about each
       // warp's mean + n_w (mean_w - mean)^2
-      if (lane == 0) buf[slot][warp] = make_float2(s, q);
+      if (lane == 0) buf[slot][warp] = make_float2(sum, q);
       __syncthreads();
       float S = 0.f, Q = 0.f;
 #pragma unroll
       for (int w = 0; w < W; ++w) S += buf[slot][w].x;
-      const float m = S / static_cast<float>(D);
+      const float m = S * inv_d;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        Q += buf[slot][w].y;
-        if (layer) {
-          // columns of warp w: 8 per lane and full group, fewer in the last
-          int nw = 0;
-#pragma unroll
-          for (int v = 0; v < NV; ++v) nw += min(max(D / 8 - v * G - w * 32, 0), 32);
-          const float nf = 8.f * static_cast<float>(nw);
-          const float d = nw > 0 ? buf[slot][w].x / nf - m : 0.f;
-          Q = fmaf(nf * d, d, Q);
-        }
+        const float2 p = buf[slot][w], n = cols[w];
+        const float d = fmaf(p.x, n.y, -m);
+        Q += fmaf(layer ? n.x * d : 0.f, d, p.y);
       }
       slot ^= 1;
       mean = layer ? m : 0.f;
       q = Q;
     }
-    return make_float2(mean, 1.f / sqrtf(q / static_cast<float>(D) + eps));
+    const float f = rsqrtf(fmaf(q, inv_d, eps));
+    return make_float2(f, -mean * f);
   }
 
   // largest bf16 magnitude of the row, as bits
-  __device__ __forceinline__ uint32_t amax(uint32_t m, int warp, int lane) {
+  __device__ __forceinline__ uint32_t amax(uint32_t m) {
     m = __reduce_max_sync(0xffffffffu, m);
     if (W > 1) {
       if (lane == 0) buf[slot][warp].x = __uint_as_float(m);
@@ -168,36 +163,43 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
   constexpr int G = 32 * W;                   // threads per row
   constexpr int kRows = (W == 1 ? 128 : G) / G;  // rows a CTA works on at a time
   __shared__ float2 buf[2][16];
+  __shared__ float2 cols[16];
   if (*(volatile const int *)p.status != kDevOk) return;
   const int t = threadIdx.x % G, warp = t >> 5, lane = t & 31;
   const int D = p.D, ng = D / 8;
   const int nv = t < ng ? (ng - 1 - t) / G + 1 : 0;  // column groups of this thread
-  RowStats<W> st{buf};
+  if (threadIdx.x < W) {
+    int n = 0;
+    for (int v = 0; v < NV; ++v) n += min(max(ng - v * G - static_cast<int>(threadIdx.x) * 32, 0), 32);
+    cols[threadIdx.x] = make_float2(8.f * n, n > 0 ? 1.f / (8.f * n) : 0.f);
+  }
+  __syncthreads();
+  RowStats<W, NV> st{buf, cols, 1.f / static_cast<float>(D), p.eps, nv, warp, lane};
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   // The next row's loads are issued before the current row's arithmetic: registers hold one
   // row of inputs in flight per thread.
   Raw8<R32> res[NV];
   Raw8<Y32> y[NV];
+  const bool has_y = p.y != nullptr;
   auto fetch = [&](int64_t row) {
     if (row >= p.T) return;
-    const int64_t base = row * D;
+    const int64_t base = row * D + t * 8;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       if (v < NV - 1 || v < nv) {  // only a thread's last group may be missing
-        res[v] = raw8<R32>(p.res, base + (v * G + t) * 8);
-        if (p.y != nullptr) y[v] = raw8<Y32>(p.y, base + (v * G + t) * 8);
+        res[v] = raw8<R32>(p.res, base + v * G * 8);
+        if (has_y) y[v] = raw8<Y32>(p.y, base + v * G * 8);
       }
     }
   };
   int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G;
   fetch(row);
   for (; row < p.T; row += step) {
-    float r[NV][8], a0[NV][8];
-    const bool has_y = p.y != nullptr;
+    float2 r[NV][4], x[NV][4];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       if (has_y) unpack8<Y32>(y[v], r[v]);
-      unpack8<R32>(res[v], a0[v]);
+      unpack8<R32>(res[v], x[v]);
     }
     fetch(row + step);
     int b = 0;
@@ -205,84 +207,85 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
       b = sample_of(p.offsets, p.B, row);
       if (b < 0) continue;  // the same for all threads of the row
     }
-    const int64_t mod = static_cast<int64_t>(b) * p.ld_mod;
-    const int64_t base = row * D;
+    const int64_t mod = static_cast<int64_t>(b) * p.ld_mod + t * 8;
+    const int64_t base = row * D + t * 8;
+    const float2 rs = both(p.res_scale);
     if (has_y) {
-      float2 ms = make_float2(0.f, 1.f);
-      if (p.post_norm != kNormNone)
-        ms = st.template norm<NV>(r, nv, warp, lane, G, D, p.post_norm == kNormLayer, p.eps);
+      if (p.post_norm != kNormNone) {
+        const float2 f = st.norm(r, p.post_norm == kNormLayer);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          float2 a[4];
+          if (p.post_weight != nullptr && (v < NV - 1 || v < nv)) load8(p.post_weight, 0, (v * G + t) * 8, a);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            r[v][e] = fma2(r[v][e], both(f.x), both(f.y));
+            if (p.post_weight != nullptr) r[v][e] = mul2(r[v][e], a[e]);
+          }
+        }
+      }
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (v < NV - 1 || v < nv) {
-          const int c = (v * G + t) * 8;
-          float a[8];
-          if (p.post_norm != kNormNone) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) r[v][e] = (r[v][e] - ms.x) * ms.y;
-            if (p.post_weight != nullptr) {
-              load8(p.post_weight, 0, c, a);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) r[v][e] *= a[e];
-            }
-          }
+          float2 a[4];
           if (p.gate != nullptr) {
-            load8(p.gate, p.mod_f32, mod + c, a);
+            load8(p.gate, p.mod_f32, mod + v * G * 8, a);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[v][e] *= a[e];
+            for (int e = 0; e < 4; ++e) r[v][e] = mul2(r[v][e], a[e]);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r[v][e] = fmaf(p.res_scale, a0[v][e], r[v][e]);
+          for (int e = 0; e < 4; ++e) r[v][e] = fma2(rs, x[v][e], r[v][e]);
         }
     } else {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[v][e] = p.res_scale * a0[v][e];
+        for (int e = 0; e < 4; ++e) r[v][e] = mul2(rs, x[v][e]);
     }
     if (p.res_out != nullptr) {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (v < NV - 1 || v < nv) {
-          const int64_t i = base + (v * G + t) * 8;
+          const int64_t i = base + v * G * 8;
           if (R32) {
             float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.res_out) + i);
-            o[0] = make_float4(r[v][0], r[v][1], r[v][2], r[v][3]);
-            o[1] = make_float4(r[v][4], r[v][5], r[v][6], r[v][7]);
+            o[0] = make_float4(r[v][0].x, r[v][0].y, r[v][1].x, r[v][1].y);
+            o[1] = make_float4(r[v][2].x, r[v][2].y, r[v][3].x, r[v][3].y);
           } else {
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.res_out) + i) = pack8(r[v]);
           }
         }
     }
     if (p.out == nullptr) continue;
-    const float2 ms = st.template norm<NV>(r, nv, warp, lane, G, D, p.norm == kNormLayer, p.eps);
+    const float2 f = st.norm(r, p.norm == kNormLayer);
     uint4 h[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       h[v] = make_uint4(0, 0, 0, 0);
       if (v < NV - 1 || v < nv) {
         const int c = (v * G + t) * 8;
-        float a[8];
+        float2 a[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[v][e] = (r[v][e] - ms.x) * ms.y;
+        for (int e = 0; e < 4; ++e) r[v][e] = fma2(r[v][e], both(f.x), both(f.y));
         if (p.weight != nullptr) {
           load8(p.weight, 0, c, a);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r[v][e] *= a[e];
+          for (int e = 0; e < 4; ++e) r[v][e] = mul2(r[v][e], a[e]);
         }
         if (p.bias != nullptr) {
           load8(p.bias, 0, c, a);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r[v][e] += a[e];
+          for (int e = 0; e < 4; ++e) r[v][e] = add2(r[v][e], a[e]);
         }
         if (p.scale != nullptr) {
-          load8(p.scale, p.mod_f32, mod + c, a);
+          load8(p.scale, p.mod_f32, mod + v * G * 8, a);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r[v][e] = fmaf(r[v][e], a[e], r[v][e]);
+          for (int e = 0; e < 4; ++e) r[v][e] = fma2(r[v][e], a[e], r[v][e]);
         }
         if (p.shift != nullptr) {
-          load8(p.shift, p.mod_f32, mod + c, a);
+          load8(p.shift, p.mod_f32, mod + v * G * 8, a);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r[v][e] += a[e];
+          for (int e = 0; e < 4; ++e) r[v][e] = add2(r[v][e], a[e]);
         }
         h[v] = pack8(r[v]);
       }
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (v < NV - 1 || v < nv)
-          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + base + (v * G + t) * 8) = h[v];
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + base + v * G * 8) = h[v];
       continue;
     }
     // quantised rows of the bf16 values in h
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
       m[v] = amax_fold(amax_bf16x2(amax_bf16x2(amax_bf16x2(amax_bf16x2(0, h[v].x), h[v].y), h[v].z), h[v].w));
       row_max = max(row_max, m[v]);
     }
-    if (p.out_format != kOutMxfp4) row_max = st.amax(row_max, warp, lane);
+    if (p.out_format != kOutMxfp4) row_max = st.amax(row_max);
     if (p.out_format == kOutE4m3) {
       const float amax = __uint_as_float(row_max << 16);
       const float inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 1.f;
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
             const uint32_t c1 = __nv_cvt_float_to_fp8(__fmul_rn(bf16_hi(w[e]), inv), __NV_SATFINITE, __NV_E4M3);
             o[e >> 1] |= (c0 | c1 << 8) << (16 * (e & 1));
           }
-          *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + base + (v * G + t) * 8) = make_uint2(o[0], o[1]);
+          *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + base + v * G * 8) = make_uint2(o[0], o[1]);
         }
       continue;
     }
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
     float rs_inv = 1.f;
     if (nv4) {
       const float rs = nvfp4_row_scale(row_max);
-      rs_inv = row_max >= kBf16Inf ? 0.f : __frcp_rn(rs);
+      rs_inv = nvfp4_row_inv(row_max);
       if (t == 0) p.out_row_scales[row] = rs;
     }
     const int64_t tiles = fp4_scale_tiles(D, nv4 ? kNvfp4 : kMxfp4);
@@ -345,19 +348,17 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
         sb = mxfp4_block_scale(am, &inv);
       }
       if (g >= ng) sb = 0;
-      const int kl = nv4 ? 2 : 4;  // lanes per block
-      uint32_t word = sb;
-#pragma unroll
-      for (int i = 1; i < 4; ++i) word |= __shfl_down_sync(0xffffffffu, sb, i * kl) << (8 * i);
-      if ((lane & (4 * kl - 1)) == 0 && g < pad_ng)
-        *reinterpret_cast<uint32_t *>(p.out_scales + fp4_scale_offset(row, g / kl, tiles)) = word;
+      const int kl = nv4 ? 2 : 4;  // lanes per block, the first of them writes its scale byte
+      if ((lane & (kl - 1)) == 0 && g < pad_ng)
+        p.out_scales[fp4_scale_offset(row, g / kl, tiles)] = static_cast<uint8_t>(sb);
       if (g < ng) {
         const uint32_t w[4] = {h[v].x, h[v].y, h[v].z, h[v].w};
         float q[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          q[2 * e] = nv4 ? e2m1_grid(bf16_lo(w[e]), inv) : bf16_lo(w[e]) * inv;
-          q[2 * e + 1] = nv4 ? e2m1_grid(bf16_hi(w[e]), inv) : bf16_hi(w[e]) * inv;
+          const float2 u = make_float2(bf16_lo(w[e]), bf16_hi(w[e]));
+          const float2 d = nv4 ? e2m1_grid(u, inv) : mul2(u, both(inv));
+          q[2 * e] = d.x, q[2 * e + 1] = d.y;
         }
         static_cast<uint32_t *>(p.out)[row * (D / 8) + g] = e2m1x8(q);
       }
