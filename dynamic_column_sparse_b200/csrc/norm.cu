@@ -14,10 +14,11 @@
 // partial sums of a row's warps joined through shared memory by the pairwise
 // rule for means and squares, so no large mean cancels.
 //
-// A row is held by one warp (up to 1024 columns) or by 4 or 16 warps of one
-// CTA, NV groups of 8 columns per thread; column group v * G + t belongs to
-// thread t, so every access is 16 bytes per lane and consecutive over a warp.
+// A row is held by one warp or by 2 to 16 warps of one CTA, NV groups of 8 columns
+// per thread; column group v * G + t belongs to thread t, so every access is 16
+// bytes per lane and consecutive over a warp.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "kernels.cuh"
@@ -38,33 +39,18 @@ __device__ __forceinline__ Raw8<F32> raw8(const void *p, int64_t i) {
   if (F32) r.w[F32 ? 1 : 0] = s[1];
   return r;
 }
+// Column e of the eight.
 template <bool F32>
-__device__ __forceinline__ void unpack8(const Raw8<F32> &r, float2 *v) {
-  if (F32) {
-    const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[F32].x, r.w[F32].y, r.w[F32].z, r.w[F32].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = make_float2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
-  } else {
-    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = make_float2(bf16_lo(w[e]), bf16_hi(w[e]));
-  }
+__device__ __forceinline__ float at8(const Raw8<F32> &r, int e) {
+  const uint4 &u = r.w[F32 ? e >> 2 : 0];
+  const int i = F32 ? e & 3 : e >> 1;
+  const uint32_t w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+  return F32 ? __uint_as_float(w) : e & 1 ? bf16_hi(w) : bf16_lo(w);
 }
 
-// Eight values of a vector shared by many rows (weights, gates, scales, shifts), bf16 or fp32.
-__device__ __forceinline__ void load8(const void *p, int f32, int64_t i, float2 *v) {
-  if (f32)
-    unpack8<true>(raw8<true>(p, i), v);
-  else
-    unpack8<false>(raw8<false>(p, i), v);
+__device__ __forceinline__ uint4 pack8(const float *v) {
+  return make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
 }
-
-__device__ __forceinline__ uint4 pack8(const float2 *v) {
-  return make_uint4(cvt_bf16x2(v[0].x, v[0].y), cvt_bf16x2(v[1].x, v[1].y), cvt_bf16x2(v[2].x, v[2].y),
-                    cvt_bf16x2(v[3].x, v[3].y));
-}
-
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -84,31 +70,30 @@ struct RowStats {
 
   // The row's mean and 1 / sqrt(variance + eps) (RMS: 0 and the root of the mean square), as the factor and
   // the addend that normalise: x * factor + addend.
-  __device__ __forceinline__ float2 norm(const float2 (&r)[NV][4], bool layer) {
+  __device__ __forceinline__ float2 norm(const float (&r)[NV][8], bool layer) {
     float mean = 0.f, sum = 0.f;
     if (layer) {
-      float2 s = both(0.f);
+      float s[2] = {0.f, 0.f};
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (v < NV - 1 || v < nv) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s = add2(s, r[v][e]);
+          for (int e = 0; e < 8; ++e) s[e & 1] += r[v][e];
         }
-      sum = warp_sum(s.x + s.y);
+      sum = warp_sum(s[0] + s[1]);
       mean = sum * cols[warp].y;
     }
-    const float2 nm = both(-mean);
-    float2 q2 = both(0.f);
+    float q2[2] = {0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v)
       if (v < NV - 1 || v < nv) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 d = add2(r[v][e], nm);
-          q2 = fma2(d, d, q2);
+        for (int e = 0; e < 8; ++e) {
+          const float d = r[v][e] - mean;
+          q2[e & 1] = fmaf(d, d, q2[e & 1]);
         }
       }
-    float q = warp_sum(q2.x + q2.y);
+    float q = warp_sum(q2[0] + q2[1]);
     if (W > 1) {
       // join the warps: squares about the row's mean = squares about each
       // warp's mean + n_w (mean_w - mean)^2
@@ -158,8 +143,95 @@ __device__ __forceinline__ int sample_of(const int32_t *off, int B, int64_t t) {
   return lo;
 }
 
-template <int W, int NV, bool R32, bool Y32>
-__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(const NormParams p) {
+// h = (r * f.x + f.y) * weight + bias, * (1 + scale) + shift, in r.
+template <int NV, bool M32>
+__device__ __forceinline__ void modulate(float (&r)[NV][8], float2 f, const NormParams &p, int nv, int G, int col,
+                                         int64_t mod) {
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    if (v < NV - 1 || v < nv) {
+      const int c = col + v * G * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[v][e] = fmaf(r[v][e], f.x, f.y);
+      if (p.weight != nullptr) {
+        const Raw8<false> a = raw8<false>(p.weight, c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[v][e] *= at8<false>(a, e);
+      }
+      if (p.bias != nullptr) {
+        const Raw8<false> a = raw8<false>(p.bias, c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[v][e] += at8<false>(a, e);
+      }
+      if (p.scale != nullptr) {
+        const Raw8<M32> a = raw8<M32>(p.scale, mod + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[v][e] = fmaf(r[v][e], at8<M32>(a, e), r[v][e]);
+      }
+      if (p.shift != nullptr) {
+        const Raw8<M32> a = raw8<M32>(p.shift, mod + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[v][e] += at8<M32>(a, e);
+      }
+    }
+}
+
+template <int NV, bool M32>
+__device__ __forceinline__ void apply_gate(float (&r)[NV][8], const NormParams &p, int nv, int G, int col, int64_t mod) {
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    if (v < NV - 1 || v < nv) {
+      const Raw8<M32> a = raw8<M32>(p.gate, mod + col + v * G * 8);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[v][e] *= at8<M32>(a, e);
+    }
+}
+
+// 4-bit codes and block scales of the bf16 row pieces h, whose magnitudes peak at m.
+// sf: where the scale of this thread's first block goes.
+template <int FMT, int NV>
+__device__ __forceinline__ void write_fp4(const uint4 (&h)[NV], const uint32_t (&m)[NV], float rs_inv, uint32_t *codes,
+                                          uint8_t *sf, int t, int G, int ng, int pad_ng) {
+  constexpr int kLanes = fp4_block(FMT) / 8;  // lanes per block, the first of them writes its scale byte
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int g = v * G + t;
+    uint32_t am = max(m[v], __shfl_xor_sync(0xffffffffu, m[v], 1));
+    if (kLanes == 4) am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+    float inv;
+    const uint32_t sb = FMT == kNvfp4 ? nvfp4_block_scale(am, rs_inv, &inv) : mxfp4_block_scale(am, &inv);
+    if ((t & (kLanes - 1)) == 0 && g < pad_ng) sf[v * (G / kLanes / 4) * 512] = static_cast<uint8_t>(g < ng ? sb : 0);
+    if (g < ng) {
+      const uint32_t w[4] = {h[v].x, h[v].y, h[v].z, h[v].w};
+      float q[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 u = make_float2(bf16_lo(w[e]), bf16_hi(w[e]));
+        const float2 d = FMT == kNvfp4 ? e2m1_grid(u, inv) : make_float2(u.x * inv, u.y * inv);
+        q[2 * e] = d.x, q[2 * e + 1] = d.y;
+      }
+      codes[v * G] = e2m1x8(q);
+    }
+  }
+}
+
+// CTAs per SM that the registers are held to (72 to 80 a thread, 128 with four column
+// groups); the grid is one wave of them, so that every CTA walks its rows with the next one
+// in flight. Measured at 20000 rows of 3072 columns: without y four warps of three column groups
+// (53.9 us; with 96 registers 61, with 64 and spills 60), with y six warps of two (81.7 us in bf16, 120 with an
+// fp32 residual; four warps of three 90 and 126).
+constexpr int ctas_per_sm(int W, int NV, bool r32, int y) {
+  const int regs = NV == 4 || (NV == 3 && W == 16 && y != 0) ? 128 : NV == 1 ? 64 : y != 0 || r32 ? 80 : NV == 2 ? 64 : 72;
+  const int n = 65536 / (32 * (W == 1 ? 4 : W) * regs);
+  return n < 1 ? 1 : n;
+}
+
+// What y is.
+enum YKind : int { kYNone = 0, kYBf16 = 1, kYF32 = 2 };
+
+template <int W, int NV, bool R32, int Y>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, ctas_per_sm(W, NV, R32, Y)) norm_residual_kernel(const NormParams p) {
+  constexpr bool has_y = Y != kYNone, Y32 = Y == kYF32;
   constexpr int G = 32 * W;                   // threads per row
   constexpr int kRows = (W == 1 ? 128 : G) / G;  // rows a CTA works on at a time
   __shared__ float2 buf[2][16];
@@ -176,11 +248,10 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
   __syncthreads();
   RowStats<W, NV> st{buf, cols, 1.f / static_cast<float>(D), p.eps, nv, warp, lane};
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  // The next row's loads are issued before the current row's arithmetic: registers hold one
-  // row of inputs in flight per thread.
+  // The next row's loads go out as soon as this row's inputs are used up, before its last
+  // norm: registers hold one row of inputs in flight per thread.
   Raw8<R32> res[NV];
   Raw8<Y32> y[NV];
-  const bool has_y = p.y != nullptr;
   auto fetch = [&](int64_t row) {
     if (row >= p.T) return;
     const int64_t base = row * D + t * 8;
@@ -195,53 +266,53 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
   int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G;
   fetch(row);
   for (; row < p.T; row += step) {
-    float2 r[NV][4], x[NV][4];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (has_y) unpack8<Y32>(y[v], r[v]);
-      unpack8<R32>(res[v], x[v]);
-    }
-    fetch(row + step);
     int b = 0;
     if (p.offsets != nullptr) {
       b = sample_of(p.offsets, p.B, row);
-      if (b < 0) continue;  // the same for all threads of the row
+      if (b < 0) {  // the same for all threads of the row
+        fetch(row + step);
+        continue;
+      }
     }
-    const int64_t mod = static_cast<int64_t>(b) * p.ld_mod + t * 8;
+    const int64_t mod = static_cast<int64_t>(b) * p.ld_mod;
     const int64_t base = row * D + t * 8;
-    const float2 rs = both(p.res_scale);
+    float r[NV][8];
     if (has_y) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[v][e] = at8<Y32>(y[v], e);
       if (p.post_norm != kNormNone) {
         const float2 f = st.norm(r, p.post_norm == kNormLayer);
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          float2 a[4];
-          if (p.post_weight != nullptr && (v < NV - 1 || v < nv)) load8(p.post_weight, 0, (v * G + t) * 8, a);
+        for (int v = 0; v < NV; ++v)
+          if (v < NV - 1 || v < nv) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            r[v][e] = fma2(r[v][e], both(f.x), both(f.y));
-            if (p.post_weight != nullptr) r[v][e] = mul2(r[v][e], a[e]);
+            for (int e = 0; e < 8; ++e) r[v][e] = fmaf(r[v][e], f.x, f.y);
+            if (p.post_weight != nullptr) {
+              const Raw8<false> a = raw8<false>(p.post_weight, (v * G + t) * 8);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) r[v][e] *= at8<false>(a, e);
+            }
           }
-        }
+      }
+      if (p.gate != nullptr) {
+        if (p.mod_f32)
+          apply_gate<NV, true>(r, p, nv, G, t * 8, mod);
+        else
+          apply_gate<NV, false>(r, p, nv, G, t * 8, mod);
       }
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        if (v < NV - 1 || v < nv) {
-          float2 a[4];
-          if (p.gate != nullptr) {
-            load8(p.gate, p.mod_f32, mod + v * G * 8, a);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) r[v][e] = mul2(r[v][e], a[e]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) r[v][e] = fma2(rs, x[v][e], r[v][e]);
-        }
+        for (int e = 0; e < 8; ++e) r[v][e] = fmaf(p.res_scale, at8<R32>(res[v], e), r[v][e]);
     } else {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[v][e] = mul2(rs, x[v][e]);
+        for (int e = 0; e < 8; ++e) r[v][e] = p.res_scale * at8<R32>(res[v], e);
     }
+    fetch(row + step);
     if (p.res_out != nullptr) {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
@@ -249,8 +320,8 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
           const int64_t i = base + v * G * 8;
           if (R32) {
             float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.res_out) + i);
-            o[0] = make_float4(r[v][0].x, r[v][0].y, r[v][1].x, r[v][1].y);
-            o[1] = make_float4(r[v][2].x, r[v][2].y, r[v][3].x, r[v][3].y);
+            o[0] = make_float4(r[v][0], r[v][1], r[v][2], r[v][3]);
+            o[1] = make_float4(r[v][4], r[v][5], r[v][6], r[v][7]);
           } else {
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.res_out) + i) = pack8(r[v]);
           }
@@ -258,50 +329,24 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
     }
     if (p.out == nullptr) continue;
     const float2 f = st.norm(r, p.norm == kNormLayer);
-    uint4 h[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      h[v] = make_uint4(0, 0, 0, 0);
-      if (v < NV - 1 || v < nv) {
-        const int c = (v * G + t) * 8;
-        float2 a[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r[v][e] = fma2(r[v][e], both(f.x), both(f.y));
-        if (p.weight != nullptr) {
-          load8(p.weight, 0, c, a);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) r[v][e] = mul2(r[v][e], a[e]);
-        }
-        if (p.bias != nullptr) {
-          load8(p.bias, 0, c, a);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) r[v][e] = add2(r[v][e], a[e]);
-        }
-        if (p.scale != nullptr) {
-          load8(p.scale, p.mod_f32, mod + v * G * 8, a);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) r[v][e] = fma2(r[v][e], a[e], r[v][e]);
-        }
-        if (p.shift != nullptr) {
-          load8(p.shift, p.mod_f32, mod + v * G * 8, a);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) r[v][e] = add2(r[v][e], a[e]);
-        }
-        h[v] = pack8(r[v]);
-      }
-    }
+    if (p.mod_f32)
+      modulate<NV, true>(r, f, p, nv, G, t * 8, mod);
+    else
+      modulate<NV, false>(r, f, p, nv, G, t * 8, mod);
     if (p.out_format == kOutBf16) {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (v < NV - 1 || v < nv)
-          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + base + v * G * 8) = h[v];
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + base + v * G * 8) = pack8(r[v]);
       continue;
     }
-    // quantised rows of the bf16 values in h
+    // quantised rows of the bf16 values
+    uint4 h[NV];
     uint32_t m[NV];
     uint32_t row_max = 0;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      h[v] = v < NV - 1 || v < nv ? pack8(r[v]) : make_uint4(0, 0, 0, 0);
       m[v] = amax_fold(amax_bf16x2(amax_bf16x2(amax_bf16x2(amax_bf16x2(0, h[v].x), h[v].y), h[v].z), h[v].w));
       row_max = max(row_max, m[v]);
     }
@@ -326,80 +371,77 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) norm_residual_kernel(co
       continue;
     }
     const bool nv4 = p.out_format == kOutNvfp4;
-    float rs_inv = 1.f;
+    const int pad_ng = (ng + 31) / 32 * 32;  // column groups that carry scale bytes: whole 256 columns
+    uint32_t *codes = static_cast<uint32_t *>(p.out) + row * ng + t;
+    uint8_t *sf = p.out_scales + fp4_scale_offset(row, t / (nv4 ? 2 : 4), fp4_scale_tiles(D, nv4 ? kNvfp4 : kMxfp4));
     if (nv4) {
-      const float rs = nvfp4_row_scale(row_max);
-      rs_inv = nvfp4_row_inv(row_max);
-      if (t == 0) p.out_row_scales[row] = rs;
-    }
-    const int64_t tiles = fp4_scale_tiles(D, nv4 ? kNvfp4 : kMxfp4);
-    const int pad_ng = (D + 255) / 256 * 32;  // column groups that carry scale bytes
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int g = v * G + t;
-      // blocks of 16 or 32 columns: 2 or 4 neighbouring lanes
-      uint32_t am = max(m[v], __shfl_xor_sync(0xffffffffu, m[v], 1));
-      float inv;
-      uint32_t sb;
-      if (nv4) {
-        sb = nvfp4_block_scale(am, rs_inv, &inv);
-      } else {
-        am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-        sb = mxfp4_block_scale(am, &inv);
-      }
-      if (g >= ng) sb = 0;
-      const int kl = nv4 ? 2 : 4;  // lanes per block, the first of them writes its scale byte
-      if ((lane & (kl - 1)) == 0 && g < pad_ng)
-        p.out_scales[fp4_scale_offset(row, g / kl, tiles)] = static_cast<uint8_t>(sb);
-      if (g < ng) {
-        const uint32_t w[4] = {h[v].x, h[v].y, h[v].z, h[v].w};
-        float q[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 u = make_float2(bf16_lo(w[e]), bf16_hi(w[e]));
-          const float2 d = nv4 ? e2m1_grid(u, inv) : mul2(u, both(inv));
-          q[2 * e] = d.x, q[2 * e + 1] = d.y;
-        }
-        static_cast<uint32_t *>(p.out)[row * (D / 8) + g] = e2m1x8(q);
-      }
+      if (t == 0) p.out_row_scales[row] = nvfp4_row_scale(row_max);
+      write_fp4<kNvfp4, NV>(h, m, nvfp4_row_inv(row_max), codes, sf, t, G, ng, pad_ng);
+    } else {
+      write_fp4<kMxfp4, NV>(h, m, 1.f, codes, sf, t, G, ng, pad_ng);
     }
   }
 }
 
-template <int W, int NV>
-void launch_nv(const NormParams &p, unsigned blocks, cudaStream_t s) {
-  const unsigned threads = W == 1 ? 128 : 32 * W;
-  if (p.res_f32) {
-    if (p.y_f32) norm_residual_kernel<W, NV, true, true><<<blocks, threads, 0, s>>>(p);
-    else norm_residual_kernel<W, NV, true, false><<<blocks, threads, 0, s>>>(p);
-  } else {
-    if (p.y_f32) norm_residual_kernel<W, NV, false, true><<<blocks, threads, 0, s>>>(p);
-    else norm_residual_kernel<W, NV, false, false><<<blocks, threads, 0, s>>>(p);
-  }
-}
-
-template <int W>
-cudaError_t launch_w(const NormParams &p, cudaStream_t s) {
-  const int need = (p.D / 8 + 32 * W - 1) / (32 * W);
+template <int W, int NV, bool R32, int Y>
+void launch_types(const NormParams &p, cudaStream_t s) {
   const int rows = W == 1 ? 4 : 1;
-  // resident CTAs, so that each prefetches its next row (W = 16: one or two per SM)
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((p.T + rows - 1) / rows, 148 * (W == 16 ? 2 : 6)));
-  switch (need) {
-    case 1: launch_nv<W, 1>(p, blocks, s); break;
-    case 2: launch_nv<W, 2>(p, blocks, s); break;
-    case 3: launch_nv<W, 3>(p, blocks, s); break;
-    default: launch_nv<W, 4>(p, blocks, s); break;
-  }
-  return cudaGetLastError();
+  const int64_t blocks = std::min<int64_t>((p.T + rows - 1) / rows, 148 * ctas_per_sm(W, NV, R32, Y));
+  norm_residual_kernel<W, NV, R32, Y><<<static_cast<unsigned>(blocks), W == 1 ? 128 : 32 * W, 0, s>>>(p);
+}
+
+// The kernel takes all but a thread's last column group for granted: each width goes to
+// the form whose groups it fills but for the last.
+//
+// Without y: up to three column groups per thread (four at the largest widths).
+template <bool R32>
+void launch_plain(const NormParams &p, cudaStream_t s) {
+  const int ng = p.D / 8;
+  auto by_nv = [&](auto w) {
+    constexpr int W = decltype(w)::value;
+    if (ng <= 32 * W) launch_types<W, 1, R32, kYNone>(p, s);
+    else if (ng <= 64 * W) launch_types<W, 2, R32, kYNone>(p, s);
+    else launch_types<W, 3, R32, kYNone>(p, s);
+  };
+  if (ng <= 96) by_nv(std::integral_constant<int, 1>());
+  else if (ng <= 192) by_nv(std::integral_constant<int, 2>());
+  else if (ng <= 384) by_nv(std::integral_constant<int, 4>());
+  else if (ng <= 768) by_nv(std::integral_constant<int, 8>());
+  else if (ng <= 1536) by_nv(std::integral_constant<int, 16>());
+  else launch_types<16, 4, R32, kYNone>(p, s);
+}
+
+// With y: up to two column groups per thread (three and four at the largest widths).
+template <bool R32, int Y>
+void launch_gated(const NormParams &p, cudaStream_t s) {
+  const int ng = p.D / 8;
+  if (ng <= 32) launch_types<1, 1, R32, Y>(p, s);
+  else if (ng <= 64) launch_types<1, 2, R32, Y>(p, s);
+  else if (ng <= 128) launch_types<2, 2, R32, Y>(p, s);
+  else if (ng <= 256) launch_types<4, 2, R32, Y>(p, s);
+  else if (ng <= 384) launch_types<6, 2, R32, Y>(p, s);
+  else if (ng <= 512) launch_types<8, 2, R32, Y>(p, s);
+  else if (ng <= 768) launch_types<12, 2, R32, Y>(p, s);
+  else if (ng <= 1024) launch_types<16, 2, R32, Y>(p, s);
+  else if (ng <= 1536) launch_types<16, 3, R32, Y>(p, s);
+  else launch_types<16, 4, R32, Y>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_residual(const NormParams &p, cudaStream_t s) {
   if (p.T <= 0) return cudaSuccess;
-  if (p.D <= 32 * 8 * 4) return launch_w<1>(p, s);
-  if (p.D <= 128 * 8 * 4) return launch_w<4>(p, s);
-  return launch_w<16>(p, s);
+  if (p.y == nullptr) {
+    if (p.res_f32) launch_plain<true>(p, s);
+    else launch_plain<false>(p, s);
+  } else if (p.res_f32) {
+    if (p.y_f32) launch_gated<true, kYF32>(p, s);
+    else launch_gated<true, kYBf16>(p, s);
+  } else {
+    if (p.y_f32) launch_gated<false, kYF32>(p, s);
+    else launch_gated<false, kYBf16>(p, s);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace cm
