@@ -496,20 +496,6 @@ def _pick(table, key, name):
         raise ValueError(f"{name} must be one of {', '.join(map(str, table))}, got {key!r}") from None
 
 
-def _here(t, name, dtypes, shape, dev):
-    """A contiguous CUDA tensor of one of ``dtypes`` and of ``shape``, on ``dev``."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if not t.is_cuda or t.device != dev:
-        raise ValueError(f"{name} must be on {dev if dev.type == 'cuda' else 'a CUDA device'}, is on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-
-
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _U8 = (torch.uint8,)
@@ -517,25 +503,75 @@ _I32 = (torch.int32,)
 _BF16_F32 = (torch.bfloat16, torch.float32)
 
 
+def _device_of(t, name, dtypes) -> int:
+    """Ordinal of the CUDA device of a 2-D tensor of one of ``dtypes``."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return dev
+
+
+def _here(t, name, dtypes, shape, dev) -> int:
+    """Address of a contiguous tensor of one of ``dtypes`` and of ``shape`` on device ordinal ``dev``."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on CUDA device {dev}, is on {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 def _empty(shape, dtype, dev, stream):
-    """Uninitialised device memory that belongs to the stream that will use it."""
+    """Uninitialised memory on device ordinal ``dev`` that belongs to the stream that will use it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+
+
+# the current stream's handle without building a Stream object (microseconds, on every call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _call(dev, stream, fn, *args):
-    """Runs a C entry point (stream last) with ``dev`` current, on ``stream`` or dev's current stream."""
+    """Runs a C entry point (stream last) with device ordinal ``dev`` current, on ``stream`` or dev's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, stream.cuda_stream))
+        handle = _raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on CUDA device {dev}")
+    else:
+        handle = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, stream.cuda_stream))
+            st = fn(*args, handle)
+    if st != OK:
+        _check(st)
+
+
+def _fp4_scale_bytes(rows, cols, f):
+    return (rows + 127) // 128 * ((cols + 255) // 256) * (2048 if f == NVFP4 else 1024)
+
+
+def _fp4_sizes(rows, cols, fmt):
+    """(format, bytes of codes, of block scales, of row scales) of rows x cols 4-bit values, each from a
+    256-byte boundary when laid one after the other."""
+    f = _pick(_FP4_FORMATS, fmt, "fmt")
+    if not 0 <= rows <= 1 << 30 or not 32 <= cols <= 65536 or cols % 32:
+        raise ValueError(f"{rows} rows x {cols} columns: columns must be a multiple of 32 in [32, 65536]")
+    return (f, (rows * (cols // 2) + 255) // 256 * 256, _fp4_scale_bytes(rows, cols, f),
+            (rows * 4 + 255) // 256 * 256 if f == NVFP4 else 0)
 
 
 class Fp4Rows:
@@ -544,74 +580,103 @@ class Fp4Rows:
     them), ``row_scales`` fp32 [rows] (nvfp4; None for mxfp4). The header of the C ABI defines both
     formats and the order of the scales."""
 
-    __slots__ = ("codes", "scales", "row_scales", "fmt", "rows", "cols", "args")
+    __slots__ = ("_codes", "_scales", "_row_scales", "_buf", "fmt", "rows", "cols", "device_index", "args")
 
     def __init__(self, codes, scales, row_scales, fmt, rows, cols):
-        f = _pick(_FP4_FORMATS, fmt, "fmt")
-        need = fp4_scale_bytes(rows, cols, fmt)
-        dev = getattr(codes, "device", None)
-        _here(codes, "codes", _U8, (rows, cols // 2), dev)
-        if not isinstance(scales, torch.Tensor) or scales.numel() != need:
-            raise ValueError(f"scales must hold {need} bytes")
-        _here(scales, "scales", _U8, scales.shape, dev)
-        if f == NVFP4:
-            _here(row_scales, "row_scales", _F32, (rows,), dev)
-        elif row_scales is not None:
+        f, _, n, _ = _fp4_sizes(rows, cols, fmt)
+        if not isinstance(codes, torch.Tensor):
+            raise TypeError("codes must be a torch.Tensor")
+        dev = codes.get_device()
+        if dev < 0:
+            raise ValueError("codes must be on a CUDA device")
+        if not isinstance(scales, torch.Tensor) or scales.numel() != n:
+            raise ValueError(f"scales must hold {n} bytes")
+        if f == MXFP4 and row_scales is not None:
             raise ValueError("mxfp4 rows have no row scales")
-        self.codes, self.scales, self.row_scales = codes, scales, row_scales
-        self.fmt, self.rows, self.cols = fmt, rows, cols
-        self.args = Fp4Args(rows, cols, f, codes.data_ptr(), scales.data_ptr(),
-                            None if row_scales is None else row_scales.data_ptr())
+        self.args = Fp4Args(rows, cols, f, _here(codes, "codes", _U8, (rows, cols // 2), dev),
+                            _here(scales, "scales", _U8, scales.shape, dev),
+                            _here(row_scales, "row_scales", _F32, (rows,), dev) if f == NVFP4 else None)
+        self._codes, self._scales, self._row_scales, self._buf = codes, scales, row_scales, None
+        self.fmt, self.rows, self.cols, self.device_index = fmt, rows, cols, dev
+
+    @classmethod
+    def _empty(cls, rows, cols, fmt, dev, stream):
+        """Uninitialised rows in one allocation; the tensors over its parts are made when asked for."""
+        f, codes, scales, rs = _fp4_sizes(rows, cols, fmt)
+        q = cls.__new__(cls)
+        q._buf = _empty((codes + scales + rs,), torch.uint8, dev, stream)
+        q._codes = q._scales = q._row_scales = None
+        q.fmt, q.rows, q.cols, q.device_index = fmt, rows, cols, dev
+        at = q._buf.data_ptr()
+        q.args = Fp4Args(rows, cols, f, at, at + codes, at + codes + scales if f == NVFP4 else None)
+        return q
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._buf[:self.rows * (self.cols // 2)].view(self.rows, self.cols // 2)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            _, c, n, _ = _fp4_sizes(self.rows, self.cols, self.fmt)
+            self._scales = self._buf[c:c + n]
+        return self._scales
+
+    @property
+    def row_scales(self):
+        if self._row_scales is None and self.fmt == "nvfp4":
+            _, c, n, _ = _fp4_sizes(self.rows, self.cols, self.fmt)
+            self._row_scales = self._buf[c + n:c + n + 4 * self.rows].view(torch.float32)
+        return self._row_scales
 
     @property
     def device(self):
-        return self.codes.device
+        return torch.device("cuda", self.device_index)
 
 
 def fp4_scale_bytes(rows: int, cols: int, fmt: str) -> int:
     """Bytes of the block scales of rows x cols 4-bit values."""
-    if not 0 <= rows <= 1 << 30 or not 32 <= cols <= 65536 or cols % 32:
-        raise ValueError(f"{rows} rows x {cols} columns: columns must be a multiple of 32 in [32, 65536]")
-    return int(load_library().chipmunk_fp4_scale_bytes(rows, cols, _pick(_FP4_FORMATS, fmt, "fmt")))
+    return _fp4_sizes(rows, cols, fmt)[2]
 
 
 def empty_fp4_rows(rows: int, cols: int, fmt: str, device, stream=None) -> Fp4Rows:
     """Uninitialised 4-bit rows for a quantising call to fill."""
     dev = torch.device(device)
-    n = fp4_scale_bytes(rows, cols, fmt)
-    return Fp4Rows(_empty((rows, cols // 2), torch.uint8, dev, stream), _empty((n,), torch.uint8, dev, stream),
-                   _empty((rows,), torch.float32, dev, stream) if fmt == "nvfp4" else None, fmt, rows, cols)
+    if dev.type != "cuda":
+        raise ValueError(f"device must be a CUDA device, got {dev}")
+    return Fp4Rows._empty(rows, cols, fmt, torch.cuda.current_device() if dev.index is None else dev.index, stream)
 
 
 def quantize_fp4_rows(x, fmt="nvfp4", out: Fp4Rows | None = None, stream=None) -> Fp4Rows:
     """Rows of bf16 x [R][C] to 4-bit microscaled rows (C a multiple of 32)."""
     lib = load_library()
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError("x must be a 2-D tensor")
+    dev = _device_of(x, "x", _BF16)
     R, C = x.shape
-    _here(x, "x", _BF16, (R, C), x.device)
+    px = _here(x, "x", _BF16, (R, C), dev)
     if out is None:
-        out = empty_fp4_rows(R, C, fmt, x.device, stream)
-    elif (out.rows, out.cols, out.fmt) != (R, C, fmt) or out.device != x.device:
-        raise ValueError(f"out holds {out.rows} x {out.cols} {out.fmt} on {out.device}, x needs {R} x {C} {fmt}")
-    _call(x.device, stream, lib.chipmunk_quantize_fp4_rows, x.data_ptr(), ctypes.byref(out.args))
+        out = Fp4Rows._empty(R, C, fmt, dev, stream)
+    elif (out.rows, out.cols, out.fmt, out.device_index) != (R, C, fmt, dev):
+        raise ValueError(f"out holds {out.rows} x {out.cols} {out.fmt} on {out.device}, x needs {R} x {C} {fmt} on {x.device}")
+    _call(dev, stream, lib.chipmunk_quantize_fp4_rows, px, out.args)
     return out
 
 
 def dequantize_fp4_rows(q: Fp4Rows, out=None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """The values that 4-bit rows stand for, [R][C] in bf16 (exact) or fp32."""
     lib = load_library()
+    dev = q.device_index
     if out is None:
-        out = _empty((q.rows, q.cols), dtype, q.device, stream)
-    _here(out, "out", _BF16_F32, (q.rows, q.cols), q.device)
-    _call(q.device, stream, lib.chipmunk_dequantize_fp4_rows, ctypes.byref(q.args), _TYPES[out.dtype], out.data_ptr())
+        out = _empty((q.rows, q.cols), dtype, dev, stream)
+    po = _here(out, "out", _BF16_F32, (q.rows, q.cols), dev)
+    _call(dev, stream, lib.chipmunk_dequantize_fp4_rows, q.args, _TYPES[out.dtype], po)
     return out
 
 
 def linear_fp4_workspace_bytes(T: int, K: int, fmt: str) -> int:
     """Workspace of a linear_fp4 call that quantises its x (none for quantised x)."""
-    w = Fp4Args(8, K, _pick(_FP4_FORMATS, fmt, "fmt"), 16, 16, 16)
-    return workspace_bytes(OP_LINEAR_FP4, LinearFp4Args(T, 8, 0, 0, 16, Fp4Args(), w, None, None))
+    return sum(_fp4_sizes(T, K, fmt)[1:])
 
 
 def linear_fp4(x, w: Fp4Rows, bias=None, out=None, act="none", out_dtype=torch.bfloat16, workspace=None, stream=None):
@@ -619,37 +684,34 @@ def linear_fp4(x, w: Fp4Rows, bias=None, out=None, act="none", out_dtype=torch.b
     Fp4Rows [T][K], w Fp4Rows [N][K], bias bf16 [N], out [T][N] bf16 or fp32. Calls that run at
     the same time, captured ones included, must not share a workspace."""
     lib = load_library()
-    dev, N, K = w.device, w.rows, w.cols
-    a = LinearFp4Args()
+    dev, N, K = w.device_index, w.rows, w.cols
+    px = pw = None
+    ws_bytes = 0
     if isinstance(x, Fp4Rows):
         T = x.rows
-        if x.cols != K or x.fmt != w.fmt or x.device != dev:
-            raise ValueError(f"x holds {x.cols} columns of {x.fmt} on {x.device}, w {K} of {w.fmt} on {dev}")
-        a.xq = x.args
-        need = 0
+        if x.cols != K or x.fmt != w.fmt or x.device_index != dev:
+            raise ValueError(f"x holds {x.cols} columns of {x.fmt} on {x.device}, w {K} of {w.fmt} on {w.device}")
+        xq = x.args
     else:
         if not isinstance(x, torch.Tensor) or x.dim() != 2:
             raise ValueError("x must be a 2-D tensor or Fp4Rows")
         T = x.shape[0]
-        _here(x, "x", _BF16, (T, K), dev)
-        a.x = x.data_ptr()
-        need = -1
-    if bias is not None:
-        _here(bias, "bias", _BF16, (N,), dev)
-        a.bias = bias.data_ptr()
+        px = _here(x, "x", _BF16, (T, K), dev)
+        xq = Fp4Args()
+        if workspace is None:
+            ws_bytes = linear_fp4_workspace_bytes(T, K, w.fmt)
+            workspace = _empty((ws_bytes,), torch.uint8, dev, stream)
+        else:
+            if workspace.get_device() != dev or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be a contiguous tensor on {w.device}")
+            ws_bytes = workspace.numel() * workspace.element_size()
+        pw = workspace.data_ptr()
+    pb = None if bias is None else _here(bias, "bias", _BF16, (N,), dev)
     if out is None:
         out = _empty((T, N), out_dtype, dev, stream)
-    _here(out, "out", _BF16_F32, (T, N), dev)
-    a.T, a.N, a.act, a.out_type = T, N, _pick(_ACTS, act, "act"), _TYPES[out.dtype]
-    a.w, a.out = w.args, out.data_ptr()
-    ws_bytes = 0
-    if need:
-        if workspace is None:
-            workspace = _empty((workspace_bytes(OP_LINEAR_FP4, a),), torch.uint8, dev, stream)
-        elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _call(dev, stream, lib.chipmunk_linear_fp4, ctypes.byref(a), workspace.data_ptr() if need else None, ws_bytes)
+    po = _here(out, "out", _BF16_F32, (T, N), dev)
+    a = LinearFp4Args(T, N, _pick(_ACTS, act, "act"), _TYPES[out.dtype], px, xq, w.args, pb, po)
+    _call(dev, stream, lib.chipmunk_linear_fp4, a, pw, ws_bytes)
     return out
 
 
@@ -664,70 +726,62 @@ def norm_residual(res, y=None, *, gate=None, post_norm="none", post_weight=None,
     updates in place) or when y is; h is bf16, (e4m3 codes, row scales) or Fp4Rows as out_format
     says, into ``out`` when given, or None for out_format=None."""
     lib = load_library()
-    if not isinstance(res, torch.Tensor) or res.dim() != 2:
-        raise ValueError("res must be a 2-D tensor")
-    T, D = res.shape
-    dev = res.device
-    a = NormArgs()
-    _here(res, "res", _BF16_F32, (T, D), dev)
-    a.T, a.D, a.res, a.res_type = T, D, res.data_ptr(), _TYPES[res.dtype]
-    a.post_norm, a.norm = _pick(_NORMS, post_norm, "post_norm"), _pick(_NORMS, norm, "norm")
-    a.eps, a.res_scale = eps, res_scale
+    dev = _device_of(res, "res", _BF16_F32)
+    shape = res.shape
+    T, D = shape
+    p_res = _here(res, "res", _BF16_F32, shape, dev)
+    p_y = p_out = p_sc = p_rs = None
+    y_type = 0
     if y is not None:
-        _here(y, "y", _BF16_F32, (T, D), dev)
-        a.y, a.y_type = y.data_ptr(), _TYPES[y.dtype]
+        p_y, y_type = _here(y, "y", _BF16_F32, shape, dev), _TYPES[y.dtype]
         if res_out is None:
-            res_out = _empty((T, D), res.dtype, dev, stream)
-    if res_out is not None:
-        _here(res_out, "res_out", (res.dtype,), (T, D), dev)
-        a.res_out = res_out.data_ptr()
-    for name, t in (("post_weight", post_weight), ("weight", weight), ("bias", bias)):
-        if t is not None:
-            _here(t, name, _BF16, (D,), dev)
-            setattr(a, name, t.data_ptr())
-    B = 1
+            res_out = _empty(shape, res.dtype, dev, stream)
+    p_ro = None if res_out is None else _here(res_out, "res_out", (res.dtype,), shape, dev)
+    p_pw = None if post_weight is None else _here(post_weight, "post_weight", _BF16, (D,), dev)
+    p_w = None if weight is None else _here(weight, "weight", _BF16, (D,), dev)
+    p_b = None if bias is None else _here(bias, "bias", _BF16, (D,), dev)
+    B, p_off = 1, None
     if offsets is not None:
         B = offsets.numel() - 1
         if B < 1:
             raise ValueError("offsets must hold at least two values")
-        _here(offsets, "offsets", _I32, (B + 1,), dev)
-        a.offsets = offsets.data_ptr()
-    a.B = B
+        p_off = _here(offsets, "offsets", _I32, (B + 1,), dev)
     mod_type = ld = None
+    mods = []
     for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
         if t is None:
+            mods.append(None)
             continue
         if not isinstance(t, torch.Tensor) or t.dtype not in _BF16_F32 or t.dtype != (mod_type or t.dtype):
             raise TypeError("gate, scale and shift must be tensors of one type, bfloat16 or float32")
-        if t.device != dev or t.shape != (B, D) or t.stride(1) != 1:
-            raise ValueError(f"{name} must be [{B}][{D}] on {dev} with consecutive columns, is {tuple(t.shape)} on {t.device}")
+        if t.get_device() != dev or t.shape != (B, D) or t.stride(1) != 1:
+            raise ValueError(f"{name} must be [{B}][{D}] on {res.device} with consecutive columns, is {tuple(t.shape)} on {t.device}")
         row = t.stride(0) if B > 1 else D
         if ld is not None and row != ld:
             raise ValueError("gate, scale and shift must have the same row stride")
         mod_type, ld = t.dtype, row
-        setattr(a, name, t.data_ptr())
-    if ld is not None:
-        a.mod_type, a.ld_mod = _TYPES[mod_type], ld
-    h = None
+        mods.append(t.data_ptr())
+    h, f = None, 0
     if out_format is not None:
-        f = a.out_format = _pick(_NORM_OUT, out_format, "out_format")
+        f = _pick(_NORM_OUT, out_format, "out_format")
         if f == 0:
-            h = _empty((T, D), torch.bfloat16, dev, stream) if out is None else out
-            _here(h, "out", _BF16, (T, D), dev)
-            a.out = h.data_ptr()
+            h = _empty(shape, torch.bfloat16, dev, stream) if out is None else out
+            p_out = _here(h, "out", _BF16, shape, dev)
         elif f == 1:
-            h = (_empty((T, D), torch.uint8, dev, stream), _empty((T,), torch.float32, dev, stream)) if out is None else out
-            _need_codes(h[0], "out codes", (T, D))
-            _here(h[1], "out scales", _F32, (T,), dev)
-            if h[0].device != dev:
-                raise ValueError(f"out codes must be on {dev}")
-            a.out, a.out_row_scales = h[0].data_ptr(), h[1].data_ptr()
+            h = (_empty(shape, torch.uint8, dev, stream), _empty((T,), torch.float32, dev, stream)) if out is None else out
+            _need_codes(h[0], "out codes", shape)
+            if h[0].get_device() != dev:
+                raise ValueError(f"out codes must be on {res.device}")
+            p_out, p_rs = h[0].data_ptr(), _here(h[1], "out scales", _F32, (T,), dev)
         else:
-            h = empty_fp4_rows(T, D, out_format, dev, stream) if out is None else out
-            if not isinstance(h, Fp4Rows) or (h.rows, h.cols, h.fmt) != (T, D, out_format) or h.device != dev:
-                raise ValueError(f"out must be Fp4Rows of {T} x {D} {out_format} on {dev}")
-            a.out, a.out_scales, a.out_row_scales = h.args.codes, h.args.scales, h.args.row_scales
-    _call(dev, stream, lib.chipmunk_norm_residual, ctypes.byref(a))
+            h = Fp4Rows._empty(T, D, out_format, dev, stream) if out is None else out
+            if not isinstance(h, Fp4Rows) or (h.rows, h.cols, h.fmt, h.device_index) != (T, D, out_format, dev):
+                raise ValueError(f"out must be Fp4Rows of {T} x {D} {out_format} on {res.device}")
+            p_out, p_sc, p_rs = h.args.codes, h.args.scales, h.args.row_scales
+    a = NormArgs(T, D, B, _TYPES[res.dtype], y_type, 0 if mod_type is None else _TYPES[mod_type],
+                 _pick(_NORMS, post_norm, "post_norm"), _pick(_NORMS, norm, "norm"), f, eps, res_scale, p_res, p_y, p_pw,
+                 mods[0], p_ro, p_w, p_b, mods[1], mods[2], ld or 0, p_off, p_out, p_sc, p_rs)
+    _call(dev, stream, lib.chipmunk_norm_residual, a)
     return res_out, h
 
 
@@ -737,24 +791,20 @@ def qk_norm_rope(qkv, h, q_weight, k_weight, cos, sin, pairs="interleaved", eps=
     q and k head with q_weight, k_weight bf16 [128], rotation by cos, sin fp32 [T][64]; returns q, k,
     v bf16 [T][h][128]."""
     lib = load_library()
-    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 2:
-        raise ValueError("qkv must be a 2-D tensor")
+    dev = _device_of(qkv, "qkv", _BF16)
     T, C = qkv.shape
-    dev = qkv.device
-    if qkv.dtype != torch.bfloat16:
-        raise TypeError(f"qkv must be torch.bfloat16, got {qkv.dtype}")
-    if not qkv.is_cuda or qkv.stride(1) != 1 or C < 3 * h * 128:
-        raise ValueError(f"qkv must be a CUDA tensor with consecutive columns, at least {3 * h * 128}, has shape {tuple(qkv.shape)}")
-    _here(q_weight, "q_weight", _BF16, (128,), dev)
-    _here(k_weight, "k_weight", _BF16, (128,), dev)
-    _here(cos, "cos", _F32, (T, 64), dev)
-    _here(sin, "sin", _F32, (T, 64), dev)
+    if qkv.stride(1) != 1 or C < 3 * h * 128:
+        raise ValueError(f"qkv must have consecutive columns, at least {3 * h * 128}, has shape {tuple(qkv.shape)}")
     shape = (T, h, 128)
-    q, k, v = (_empty(shape, torch.bfloat16, dev, stream) if t is None else t for t in (q, k, v))
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _here(t, name, _BF16, shape, dev)
+    if q is None:
+        q = _empty(shape, torch.bfloat16, dev, stream)
+    if k is None:
+        k = _empty(shape, torch.bfloat16, dev, stream)
+    if v is None:
+        v = _empty(shape, torch.bfloat16, dev, stream)
     a = HeadsArgs(T, qkv.stride(0) if T > 1 else 3 * h * 128, h, _pick(_PAIRS, pairs, "pairs"), eps, qkv.data_ptr(),
-                  q_weight.data_ptr(), k_weight.data_ptr(), cos.data_ptr(), sin.data_ptr(), q.data_ptr(), k.data_ptr(),
-                  v.data_ptr())
-    _call(dev, stream, lib.chipmunk_qk_norm_rope, ctypes.byref(a))
+                  _here(q_weight, "q_weight", _BF16, (128,), dev), _here(k_weight, "k_weight", _BF16, (128,), dev),
+                  _here(cos, "cos", _F32, (T, 64), dev), _here(sin, "sin", _F32, (T, 64), dev),
+                  _here(q, "q", _BF16, shape, dev), _here(k, "k", _BF16, shape, dev), _here(v, "v", _BF16, shape, dev))
+    _call(dev, stream, lib.chipmunk_qk_norm_rope, a)
     return q, k, v

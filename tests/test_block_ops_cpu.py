@@ -117,6 +117,18 @@ def test_struct_layouts_match_the_header(cm, tmp_path):
         assert int(val) == (ctypes.sizeof(py) if field == "sizeof" else getattr(py, field).offset), (cname, field)
 
 
+def test_sizes_of_the_binding_match_the_library(cm):
+    lib = cm.load_library()
+    for fmt, f in (("nvfp4", cm.NVFP4), ("mxfp4", cm.MXFP4)):
+        for rows in (1, 127, 128, 129, 4352, 118800):
+            for cols in (32, 64, 224, 256, 288, 3072, 65536):
+                assert cm.fp4_scale_bytes(rows, cols, fmt) == lib.chipmunk_fp4_scale_bytes(rows, cols, f)
+                w = cm.Fp4Args(8, cols, f, 16, 16, 16)
+                a = cm.LinearFp4Args(rows, 8, 0, 0, 16, cm.Fp4Args(), w, None, None)
+                assert cm.linear_fp4_workspace_bytes(rows, cols, fmt) == cm.workspace_bytes(cm.OP_LINEAR_FP4, a)
+    assert lib.chipmunk_fp4_scale_bytes(1, 48, 0) == 0
+
+
 def test_scale_bytes(cm):
     assert cm.fp4_scale_bytes(1, 32, "nvfp4") == 4 * 512 and cm.fp4_scale_bytes(1, 32, "mxfp4") == 2 * 512
     assert cm.fp4_scale_bytes(129, 288, "nvfp4") == 2 * 8 * 512
@@ -178,6 +190,7 @@ def test_linear_refusals(cm):
     a = _linear(cm)
     need = cm.workspace_bytes(cm.OP_LINEAR_FP4, a)
     # 40 rows of 128 bytes of codes, one tile row of scales, 40 row scales, each from a 256-byte boundary
+    # (codes to a 256-byte boundary, row scales too)
     assert need == 40 * 128 + 4 * 512 + 256 == cm.linear_fp4_workspace_bytes(40, 256, "nvfp4")
     assert cm.linear_fp4_workspace_bytes(40, 256, "mxfp4") == 40 * 128 + 2 * 512
     assert call(a, None, 0) == cm.ERR_WORKSPACE and call(a, 0x6000, need - 1) == cm.ERR_WORKSPACE
