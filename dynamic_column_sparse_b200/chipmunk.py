@@ -675,8 +675,9 @@ def dequantize_fp4_rows(q: Fp4Rows, out=None, dtype=torch.bfloat16, stream=None)
 
 
 def linear_fp4_workspace_bytes(T: int, K: int, fmt: str) -> int:
-    """Workspace of a linear_fp4 call that quantises its x (none for quantised x)."""
-    return sum(_fp4_sizes(T, K, fmt)[1:])
+    """Workspace of a linear_fp4 call that quantises its x (none for quantised x, nor for a few rows)."""
+    need = sum(_fp4_sizes(T, K, fmt)[1:])
+    return 0 if T <= 8 and T * ((K + 255) // 256 * 256) <= 8192 else need
 
 
 def linear_fp4(x, w: Fp4Rows, bias=None, out=None, act="none", out_dtype=torch.bfloat16, workspace=None, stream=None):
@@ -700,12 +701,13 @@ def linear_fp4(x, w: Fp4Rows, bias=None, out=None, act="none", out_dtype=torch.b
         xq = Fp4Args()
         if workspace is None:
             ws_bytes = linear_fp4_workspace_bytes(T, K, w.fmt)
-            workspace = _empty((ws_bytes,), torch.uint8, dev, stream)
+            if ws_bytes:
+                workspace = _empty((ws_bytes,), torch.uint8, dev, stream)
         else:
             if workspace.get_device() != dev or not workspace.is_contiguous():
                 raise ValueError(f"workspace must be a contiguous tensor on {w.device}")
             ws_bytes = workspace.numel() * workspace.element_size()
-        pw = workspace.data_ptr()
+        pw = None if workspace is None else workspace.data_ptr()
     pb = None if bias is None else _here(bias, "bias", _BF16, (N,), dev)
     if out is None:
         out = _empty((T, N), out_dtype, dev, stream)

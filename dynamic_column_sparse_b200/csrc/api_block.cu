@@ -97,13 +97,14 @@ chipmunk_status linear_maps(cm::LinearFp4Maps *m, const chipmunk_linear_fp4_args
   const uint64_t dx[] = {bytes, T}, dw[] = {bytes, N}, dsx[] = {128, tiles, (T + 127) / 128},
                  dsw[] = {128, tiles, (N + 127) / 128}, dout[] = {N, T};
   const uint64_t sb[] = {bytes}, ss[] = {512, tiles * 512}, so[] = {N * out_es};
-  const uint32_t box[] = {128, 128}, bsx[] = {128, per_stage, 1}, bsw1[] = {128, per_stage, 1},
+  const uint32_t box[] = {128, 128}, boxw[] = {128, 256}, bsx[] = {128, per_stage, 1}, bsw1[] = {128, per_stage, 1},
                  bsw2[] = {128, per_stage, 2}, bout[] = {uint32_t(128 / out_es), 32};
+  const bool wide = m->form == cm::kLinearPair || m->form == cm::kLinearWide;  // 256 columns per tile
+  CM_CHECK(cm::encode_map(&m->w, u8, a->w.codes, 2, dw, sb, m->form == cm::kLinearWide ? boxw : box, true, "w codes"));
+  CM_CHECK(cm::encode_map(&m->sw, i32, a->w.scales, 3, dsw, ss, wide ? bsw2 : bsw1, false, "w scales"));
+  if (m->form == cm::kLinearRows) return CHIPMUNK_OK;
   CM_CHECK(cm::encode_map(&m->x, u8, xq.codes, 2, dx, sb, box, true, "x codes"));
-  CM_CHECK(cm::encode_map(&m->w, u8, a->w.codes, 2, dw, sb, box, true, "w codes"));
   CM_CHECK(cm::encode_map(&m->sx, i32, xq.scales, 3, dsx, ss, bsx, false, "x scales"));
-  m->pair = cm::linear_fp4_pair(T, N);
-  CM_CHECK(cm::encode_map(&m->sw, i32, a->w.scales, 3, dsw, ss, m->pair ? bsw2 : bsw1, false, "w scales"));
   return cm::encode_map(&m->out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->out, 2,
                         dout, so, bout, true, "out");
 }
@@ -114,6 +115,7 @@ namespace cm {
 
 size_t linear_fp4_ws(const chipmunk_linear_fp4_args *a) {
   if (a->x == nullptr || a->T < 1 || !fp4_sizes_ok(a->T, a->w.cols, a->w.format)) return 0;
+  if (linear_fp4_form(a->T, a->N, a->w.cols, false) == kLinearRows) return 0;
   size_t n = round_up(size_t(a->T) * size_t(a->w.cols / 2), 256) + fp4_scale_bytes(a->T, a->w.cols, a->w.format);
   if (a->w.format == CHIPMUNK_NVFP4) n += round_up(size_t(a->T) * 4, 256);
   return n;
@@ -173,7 +175,11 @@ chipmunk_status chipmunk_linear_fp4(const chipmunk_linear_fp4_args *a, void *ws,
   const Ptr ptrs[] = {{a->x, "x", false}, {a->bias, "bias", false}, {a->out, "out", true}};
   CM_CHECK(check_ptrs(ptrs, 3));
   chipmunk_fp4_rows xq = a->xq;
-  if (a->x != nullptr) {
+  cm::LinearFp4Maps m;
+  m.form = cm::linear_fp4_form(a->T, a->N, a->w.cols, a->x == nullptr);
+  if (m.form == cm::kLinearRows) {
+    // quantised inside the product's kernel: no workspace
+  } else if (a->x != nullptr) {
     const size_t need = cm::linear_fp4_ws(a);
     if (ws == nullptr || ws_bytes < need)
       return record_errorf(CHIPMUNK_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
@@ -191,9 +197,8 @@ chipmunk_status chipmunk_linear_fp4(const chipmunk_linear_fp4_args *a, void *ws,
   CM_CHECK(cm::device_ready(&status));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f32 = a->out_type == CHIPMUNK_FP32;
-  cm::LinearFp4Maps m;
   CM_CHECK(linear_maps(&m, a, xq));
-  if (a->x != nullptr)
+  if (a->x != nullptr && m.form != cm::kLinearRows)
     CM_CUDA(cm::launch_quantize_fp4_rows(quant_params(a->x, &xq, status), s), "4-bit quantise launch");
   cm::LinearFp4Params p{int(a->T),
                         int(a->N),
@@ -204,6 +209,8 @@ chipmunk_status chipmunk_linear_fp4(const chipmunk_linear_fp4_args *a, void *ws,
                         xq.row_scales,
                         a->w.row_scales,
                         static_cast<const uint16_t *>(a->bias),
+                        static_cast<const uint16_t *>(a->x),
+                        a->out,
                         status};
   CM_CUDA(cm::launch_linear_fp4(p, m, s), "4-bit linear launch");
   return CHIPMUNK_OK;

@@ -19,6 +19,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) quantize_fp4_rows_kerne
   constexpr int G = 32 * W, kRows = W == 1 ? 4 : 1;
   constexpr int kLanes = FMT == kNvfp4 ? 1 : 2;  // lanes per block
   __shared__ uint32_t row_max[2][16];
+  allow_dependents();  // a product launched behind this kernel sets up meanwhile
   if (*(volatile const int *)p.status != kDevOk) return;
   const int t = threadIdx.x % G, lane = threadIdx.x & 31;
   const int groups = static_cast<int>(p.cols / 16);

@@ -148,17 +148,23 @@ struct LinearFp4Params {
   int gelu, out_f32;
   const float *rx, *rw;        // row scales (NVFP4)
   const uint16_t *bias;        // [N] bf16 or nullptr
+  const uint16_t *x;           // [T][K] bf16: read by the form for a few rows; for the others, not nullptr
+                               // when the codes come from a quantiser launched just before
+  void *out;                   // [T][N]
   int *status;
 };
+// The kernel's forms: a few bf16 rows quantised in place, one CTA per 128 x 128 or 128 x 256 tile, a CTA pair per
+// 256 x 256 tile.
+enum LinearFp4Form : int { kLinearRows = 0, kLinearSingle = 1, kLinearPair = 2, kLinearWide = 3 };
+LinearFp4Form linear_fp4_form(int64_t T, int64_t N, int64_t K, bool quantised);  // the form a product takes
 // Codes as rows of bytes (boxes of 128 bytes x 128 rows); block scales as 512-byte
 // tiles, [tiles of 128 rows][tiles along the columns][128 words] (boxes of one
 // stage's tiles of one row tile of x, of one or two row tiles of w); out (boxes of 128 bytes x 32
-// rows). pair: the maps are those of the form of the kernel that works in CTA pairs.
+// rows). The form for a few rows reads w and sw only.
 struct LinearFp4Maps {
   CUtensorMap x, w, sx, sw, out;
-  bool pair;
+  LinearFp4Form form;
 };
-bool linear_fp4_pair(int64_t T, int64_t N);  // which form a product of these sizes takes
 cudaError_t launch_linear_fp4(const LinearFp4Params &p, const LinearFp4Maps &m, cudaStream_t s);
 
 // ------------------------------------------------------------------ norms with gate and residual

@@ -3,10 +3,10 @@
 //   out[t][n] = act(rx[t] rw[n] sum_k x[t][k] w[n][k] + bias[n])
 // with x [T][K] and w [N][K] as codes, block scales and (NVFP4) row scales.
 //
-// Persistent, one CTA per SM. Two forms: a CTA pair (cta_group::2) on a 256 x
+// Persistent, one CTA per SM. Three forms: a CTA pair (cta_group::2) on a 256 x
 // 256 output tile, each CTA holding 128 rows of x, 128 rows of w and 128 rows of
-// the result; and one CTA on a 128 x 128 tile where the larger tiles would leave SMs
-// idle. Tiles are walked weight-slice fastest, so a row block of x is read
+// the result; and one CTA on a 128 x 256 or 128 x 128 tile where larger tiles would leave SMs
+// idle (linear_fp4_form chooses; a fourth form, below, takes a few rows). Tiles are walked weight-slice fastest, so a row block of x is read
 // from HBM once while the weights stay in L2.
 //
 // Warp 0 fills a ring of stages of 256 columns with TMA: code tiles
@@ -20,6 +20,7 @@
 // columns, which leaves 64 for the scales: the shared columns are drained first and the next
 // tile's MMAs wait for them only.
 #include <algorithm>
+#include <atomic>
 
 #include "fp4.cuh"
 #include "kernels.cuh"
@@ -31,7 +32,7 @@ namespace {
 // CG CTAs per tile; BN tile columns; 128 * CG tile rows.
 template <int CG, int BN>
 struct LinCfg {
-  static constexpr int kStages = CG == 2 ? 5 : 5;
+  static constexpr int kStages = CG == 1 && BN == 256 ? 3 : 5;
   static constexpr int kBRows = BN / CG;  // rows of w a CTA loads
   static constexpr uint32_t kABytes = 128 * 128, kBBytes = kBRows * 128;
   static constexpr uint32_t kSaBytes = 2048, kSbBytes = BN / 128 * 2048;  // MXFP4 uses half
@@ -134,24 +135,41 @@ __global__ void __launch_bounds__(320, 1)
   if (!run) {
   } else if (warp == 0) {
     const uint32_t lead = elect_lane();
+    // loads of stage kg (K block kb of a tile) into slot s: w's, or x's
+    auto load_w = [&](int s, int kb, int nt) {
+      uint8_t *b = smem + s * C::kStageBytes + C::kABytes, *sb = b + C::kBBytes + C::kSaBytes;
+      if (CG == 1 || rank == 0) mbar_arrive_expect_tx_lead(&full[s], kTx, lead);
+      const uint32_t bar = CG == 2 ? cluster_addr(&full[s], 0) : smem_u32(&full[s]);
+      tma_load_2d_lead<CG>(b, &m.w, bar, kb * 128, nt * BN + rank * C::kBRows, lead);
+      tma_load_3d_lead<CG>(sb, &m.sw, bar, 0, kb * kAtoms, nt * (BN / 128), lead);
+    };
+    auto load_x = [&](int s, int kb, int mt) {
+      uint8_t *a = smem + s * C::kStageBytes, *sa = a + C::kABytes + C::kBBytes;
+      const int xr = mt * CG + rank;  // this CTA's 128 rows of x
+      const uint32_t bar = CG == 2 ? cluster_addr(&full[s], 0) : smem_u32(&full[s]);
+      tma_load_2d_lead<CG>(a, &m.x, bar, kb * 128, xr * 128, lead);
+      tma_load_3d_lead<CG>(sa, &m.sx, bar, 0, kb * kAtoms, xr, lead);
+    };
+    // w does not wait for the quantiser of x that this kernel may have been launched behind: the ring's
+    // first turn loads it ahead
+    int ahead = 0;
+    for (int tile = first; tile < ntiles && ahead < S; tile += step)
+      for (int kb = 0; kb < nk && ahead < S; ++kb, ++ahead) load_w(ahead, kb, tile % tiles_n);
+    wait_for_primary();
     int s = 0, kg = 0;
     uint32_t ph = 1;  // parity of the wait for an empty stage
     bool ok = true;
     for (int tile = first; tile < ntiles && ok; tile += step) {
       const int mt = tile / tiles_n, nt = tile - mt * tiles_n;
-      const int xr = mt * CG + rank;  // this CTA's 128 rows of x
       for (int kb = 0; kb < nk; ++kb, ++kg) {
-        if (!wait_warp(&empty[s], ph, p.status, abort_flag)) {
-          ok = false;
-          break;
+        if (kg >= ahead) {
+          if (!wait_warp(&empty[s], ph, p.status, abort_flag)) {
+            ok = false;
+            break;
+          }
+          load_w(s, kb, nt);
         }
-        uint8_t *a = smem + s * C::kStageBytes, *b = a + C::kABytes, *sa = b + C::kBBytes, *sb = sa + C::kSaBytes;
-        if (CG == 1 || rank == 0) mbar_arrive_expect_tx_lead(&full[s], kTx, lead);
-        const uint32_t bar = CG == 2 ? cluster_addr(&full[s], 0) : smem_u32(&full[s]);
-        tma_load_2d_lead<CG>(a, &m.x, bar, kb * 128, xr * 128, lead);
-        tma_load_2d_lead<CG>(b, &m.w, bar, kb * 128, nt * BN + rank * C::kBRows, lead);
-        tma_load_3d_lead<CG>(sa, &m.sx, bar, 0, kb * kAtoms, xr, lead);
-        tma_load_3d_lead<CG>(sb, &m.sw, bar, 0, kb * kAtoms, nt * (BN / 128), lead);
+        load_x(s, kb, mt);
         if (++s == S) s = 0, ph ^= 1;
       }
     }
@@ -161,7 +179,7 @@ __global__ void __launch_bounds__(320, 1)
     const uint32_t lead = elect_lane();
     const int my_tiles = first < ntiles ? (ntiles - 1 - first) / step + 1 : 0;
     int left = my_tiles * nk;          // stages not yet looked at
-    const uint64_t desc_ab = sdesc_sw128(smem_u32(smem), 16, 1024), desc_sf = sdesc_plain(smem_u32(smem));
+    const uint64_t desc_ab = sdesc_sw128(smem_u32(smem), 16, 1024), desc_sf = sdesc_plain(smem_u32(smem), 128);
     constexpr uint32_t kSfOff = C::kABytes + C::kBBytes;
     uint32_t sf = C::kSfCol;           // columns of the next scale slot
     // copies scale tile j of stage s into the next slot; returns the slot's columns
@@ -227,6 +245,7 @@ __global__ void __launch_bounds__(320, 1)
     uint8_t *stage = smem + C::kOutOff + (warp - 2) * C::kOutBytes;
     uint32_t *cols = reinterpret_cast<uint32_t *>(smem + C::kColOff);
     int tl = 0;
+    wait_for_primary();  // the row scales of x
     // a drained accumulator (or its shared columns) goes back to the leader's MMA warp
     auto release = [&](uint64_t *bar) {
       tc_fence_before();
@@ -337,43 +356,330 @@ __global__ void __launch_bounds__(320, 1)
   }
 }
 
-template <int CG, int BN>
-cudaError_t launch_form(const LinearFp4Params &p, LinearFp4Maps m, int sms, cudaStream_t s) {
+// ------------------------------------------------------------------ a few rows
+
+// Products with at most 8 rows, and few enough columns to quantise them anew in every CTA
+// (16 of a row per thread and step, at most kRowItems steps): one launch and no workspace.
+// Bound by reading w once, in practice by launch and pipeline latency: 1 x 18432 x 3072
+// NVFP4 moves 32 MB (4.9 us at the copy rate).
+//
+// Warps 2-9 quantise x into shared memory while warp 0 already fills the ring with w;
+// then warps 4 and 8, whose TMEM lanes hold the rows, are the epilogue. Only one 8-row
+// swizzle atom of x exists per stage: the descriptors' stride between 8-row groups is 0, so
+// all 128 rows of the instruction read it (and the scale copies likewise); rows from the
+// eighth on repeat the first eight, and none but the T first is stored.
+constexpr int kRowMax = 8, kRowItems = 2;
+
+constexpr int kRowStagesMax = kRowItems * 16;  // one row of as many columns: 8192
+
+struct RowCfg {
+  static constexpr int kStages = 5;
+  static constexpr uint32_t kWBytes = 128 * 128, kSwBytes = 2048;
+  static constexpr uint32_t kStageBytes = kWBytes + kSwBytes;
+  static constexpr uint32_t kXBytes = 1024, kSxBytes = 512;  // x per 256 columns: codes; scales, 128 bytes per tile
+  static constexpr uint32_t kXOff = kStages * kStageBytes;
+  static constexpr uint32_t kBarBytes = 512;
+  static constexpr uint32_t smem(int nk) { return 1024 + kXOff + nk * (kXBytes + kSxBytes) + 2 * 128 * 4 + kBarBytes; }
+  static constexpr uint32_t kSfCol = 256, kSfCols = 8;
+  static constexpr int kSfSlots = 5;
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(320, 1)
+    linear_fp4_rows_kernel(const __grid_constant__ LinearFp4Maps m, const LinearFp4Params p) {
+  using C = RowCfg;
+  constexpr int S = C::kStages;
+  constexpr bool S16 = FMT == kNvfp4;
+  constexpr int kAtoms = S16 ? 4 : 2, kPerAtom = 4 / kAtoms;
+  constexpr uint32_t kTx = C::kWBytes + kAtoms * 512;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = align_up<1024>(smem_raw);
+  const int nk = (p.K + 255) / 256;
+  uint8_t *xs = smem + C::kXOff;                    // codes, 1 KB per 256 columns
+  uint8_t *sx = xs + nk * C::kXBytes;               // scales, 128 bytes per scale tile
+  uint32_t *cols = reinterpret_cast<uint32_t *>(sx + nk * C::kSxBytes);  // [2][128]: row scale of w and bias, bf16 each
+  uint64_t *full = reinterpret_cast<uint64_t *>(cols + 2 * 128);
+  uint64_t *empty = full + S;
+  uint64_t *acc_full = empty + S;      // [2]
+  uint64_t *acc_empty = acc_full + 2;  // [2]
+  uint64_t *x_ready = acc_empty + 2;
+  uint32_t *row_max = reinterpret_cast<uint32_t *>(x_ready + 1);  // [8] bits of the rows' largest magnitudes
+  uint32_t *tmem_slot = row_max + kRowMax;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (*(volatile int *)p.status != kDevOk) return;
+  const int ntiles = (p.N + 127) / 128;
+  const int first = blockIdx.x, step = gridDim.x;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_empty[s], 2);
+    }
+    mbar_init(x_ready, 256);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (threadIdx.x < kRowMax) row_max[threadIdx.x] = 0;
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
+
+  if (warp == 0) {
+    const uint32_t lead = elect_lane();
+    int s = 0, kg = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (int tile = first; tile < ntiles && ok; tile += step) {
+      for (int kb = 0; kb < nk; ++kb, ++kg) {
+        if (!wait_warp(&empty[s], ph, p.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint8_t *b = smem + s * C::kStageBytes;
+        mbar_arrive_expect_tx_lead(&full[s], kTx, lead);
+        tma_load_2d_lead<1>(b, &m.w, smem_u32(&full[s]), kb * 128, tile * 128, lead);
+        tma_load_3d_lead<1>(b + C::kWBytes, &m.sw, smem_u32(&full[s]), 0, kb * kAtoms, tile, lead);
+        if (++s == S) s = 0, ph ^= 1;
+      }
+    }
+    if (!ok)  // gave up: let the copies in flight land before the shared memory goes away
+      for (int f = max(kg - S, 0); f < kg; ++f) mbar_drain(&full[f % S], (f / S) & 1);
+  } else if (warp == 1) {
+    const uint32_t lead = elect_lane();
+    const int my_tiles = first < ntiles ? (ntiles - 1 - first) / step + 1 : 0;
+    const uint64_t desc_w = sdesc_sw128(smem_u32(smem), 16, 1024), desc_x = sdesc_sw128(smem_u32(xs), 16, 0);
+    const uint64_t desc_sw = sdesc_plain(smem_u32(smem) + C::kWBytes, 128), desc_sx = sdesc_plain(smem_u32(sx), 0);
+    int s = 0;
+    uint32_t ph = 0, sf = C::kSfCol;
+    bool ok = wait_warp(x_ready, 0, p.status, abort_flag);
+    for (int tl = 0; tl < my_tiles && ok; ++tl) {
+      const int ab = tl & 1;
+      ok = wait_warp(&acc_empty[ab], ((tl >> 1) & 1) ^ 1, p.status, abort_flag);
+      tc_fence_after();
+      for (int kb = 0; kb < nk && ok; ++kb) {
+        ok = wait_warp(&full[s], ph, p.status, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t st = static_cast<uint64_t>((s * C::kStageBytes) >> 4);
+#pragma unroll
+        for (int j = 0; j < kAtoms; ++j) {
+          tmem_cp_scales<1>(tmem + sf, desc_sx + (kb * C::kSxBytes + j * 128) / 16, lead);
+          tmem_cp_scales<1>(tmem + sf + 4, desc_sw + st + j * 32, lead);
+#pragma unroll
+          for (int q = 0; q < kPerAtom; ++q) {
+            const int kk = j * kPerAtom + q;
+            umma_fp4<S16, 1>(tmem + ab * 128, desc_x + kb * (C::kXBytes / 16) + kk * 2, desc_w + st + kk * 2,
+                             idesc_fp4(128, 128, S16, q * 2), tmem + sf, tmem + sf + 4, (kb | kk) != 0, lead);
+          }
+          sf = sf + C::kSfCols == C::kSfCol + C::kSfSlots * C::kSfCols ? C::kSfCol : sf + C::kSfCols;
+        }
+        umma_commit_lead<1>(&empty[s], lead);
+        if (kb == nk - 1) umma_commit_lead<1>(&acc_full[ab], lead);
+        if (++s == S) s = 0, ph ^= 1;
+      }
+    }
+  } else {
+    // quantise: item i is 16 columns of a row; the columns up to a whole 256 are zeros
+    const int t = threadIdx.x - 64, groups = p.K / 16, per_row = nk * 16, items = p.T * per_row;
+    Vec32 u[kRowItems];
+    uint32_t am[kRowItems];
+#pragma unroll
+    for (int v = 0; v < kRowItems; ++v) {
+      const int i = v * 256 + t, r = i / per_row, g = i - r * per_row;
+      u[v] = i < items && g < groups ? load16x2(p.x + static_cast<int64_t>(r) * p.K + g * 16) : Vec32{};
+    }
+#pragma unroll
+    for (int v = 0; v < kRowItems; ++v) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a = amax_bf16x2(a, u[v].w[e]);
+      am[v] = amax_fold(a);
+      const int i = v * 256 + t;
+      if (S16 && i < items) atomicMax(&row_max[i / per_row], am[v]);
+    }
+    if (S16) asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll
+    for (int v = 0; v < kRowItems; ++v) {
+      const int i = v * 256 + t;
+      if (v * 256 + (t & ~31) >= items) break;  // whole warps leave together (per_row is even: pairs of lanes share a row)
+      const int r = i / per_row, g = i - r * per_row;
+      float inv;
+      uint32_t sb;
+      if (S16) {
+        sb = nvfp4_block_scale(am[v], nvfp4_row_inv(i < items ? row_max[r] : 0), &inv);
+      } else {
+        sb = mxfp4_block_scale(max(am[v], __shfl_xor_sync(0xffffffffu, am[v], 1)), &inv);
+      }
+      if (i < items) {
+        float q[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t w = u[v].w[e];
+          const float2 x = make_float2(bf16_lo(w), bf16_hi(w));
+          const float2 d = S16 ? e2m1_grid(x, inv) : make_float2(x.x * inv, x.y * inv);
+          q[2 * e] = d.x, q[2 * e + 1] = d.y;
+        }
+        const int st = g >> 4, c = g & 15;
+        *reinterpret_cast<uint2 *>(xs + st * C::kXBytes + sw128_offset(r, c >> 1) + (c & 1) * 8) =
+            make_uint2(e2m1x8(q), e2m1x8(q + 8));
+        // scale of a block: byte block % 4 of the row's 16 bytes in its scale tile
+        const int blk = S16 ? c : c >> 1;
+        if (S16 || (g & 1) == 0)
+          sx[st * C::kSxBytes + (blk >> 2) * 128 + r * 16 + (blk & 3)] = static_cast<uint8_t>(g < groups ? sb : 0);
+      }
+    }
+    fence_async_smem();
+    mbar_arrive(x_ready);
+    if ((warp & 3) == 0) {  // TMEM lanes 0-31; warp 4 takes the first 64 columns, warp 8 the others
+      const int half = warp >> 3;
+      bool ok = wait_warp(x_ready, 0, p.status, abort_flag);
+      const float rx = S16 && lane < p.T ? nvfp4_row_scale(row_max[lane & 7]) : 1.f;
+      int tl = 0;
+      for (int tile = first; tile < ntiles && ok; tile += step, ++tl) {
+        const int ab = tl & 1, n0 = tile * 128 + half * 64;
+        uint32_t *cw = cols + ab * 128 + half * 64;
+#pragma unroll
+        for (int c = lane; c < 64; c += 32) {
+          uint32_t col = 0x3f800000u;
+          if (n0 + c < p.N) {
+            if (S16) col = static_cast<uint32_t>(f32_to_bf16_bits(p.rw[n0 + c])) << 16;
+            if (p.bias != nullptr) col |= p.bias[n0 + c];
+          }
+          cw[c] = col;
+        }
+        __syncwarp();
+        ok = wait_warp(&acc_full[ab], (tl >> 1) & 1, p.status, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        float v[64];
+        tmem_ld64(tmem + ab * 128 + half * 64, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[ab]);
+#pragma unroll
+        for (int q = 0; q < 64; ++q) {
+          const uint32_t w = cw[q];
+          v[q] = fmaf(v[q], rx * bf16_hi(w), bf16_lo(w));
+          if (p.gelu) v[q] = gelu_sigmoid(v[q]);
+        }
+        if (lane < p.T) {
+          const int64_t o = static_cast<int64_t>(lane) * p.N + n0;
+#pragma unroll
+          for (int q = 0; q < 64; q += 8) {
+            if (n0 + q >= p.N) break;  // N is a multiple of 8
+            if (p.out_f32) {
+              float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + o + q);
+              d[0] = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+              d[1] = make_float4(v[q + 4], v[q + 5], v[q + 6], v[q + 7]);
+            } else {
+              *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + o + q) =
+                  make_uint4(cvt_bf16x2(v[q], v[q + 1]), cvt_bf16x2(v[q + 2], v[q + 3]),
+                             cvt_bf16x2(v[q + 4], v[q + 5]), cvt_bf16x2(v[q + 6], v[q + 7]));
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Shared-memory limit of a kernel, raised once per device.
+template <auto Kernel>
+cudaError_t allow_smem(uint32_t bytes, int dev) {
+  static std::atomic<bool> done[64];
+  if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+template <int FMT, int CG, int BN>
+cudaError_t launch_form(const LinearFp4Params &p, const LinearFp4Maps &m, int dev, int sms, cudaStream_t s) {
   using C = LinCfg<CG, BN>;
   const int64_t tiles = static_cast<int64_t>((p.T + 128 * CG - 1) / (128 * CG)) * ((p.N + BN - 1) / BN);
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(tiles, sms / CG)) * CG;
-  auto kernel = p.fmt == kNvfp4 ? linear_fp4_kernel<kNvfp4, CG, BN> : linear_fp4_kernel<kMxfp4, CG, BN>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  const cudaError_t e = allow_smem<linear_fp4_kernel<FMT, CG, BN>>(C::kSmem, dev);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CG;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  // behind its own quantiser: set up while that runs
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, sms / CG)) * CG);
   cfg.blockDim = dim3(320);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, m, p);
+  cfg.numAttrs = p.x != nullptr ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, linear_fp4_kernel<FMT, CG, BN>, m, p);
+}
+
+template <int FMT>
+cudaError_t launch_rows(const LinearFp4Params &p, const LinearFp4Maps &m, int dev, int sms, cudaStream_t s) {
+  const int nk = (p.K + 255) / 256;
+  const cudaError_t e = allow_smem<linear_fp4_rows_kernel<FMT>>(RowCfg::smem(kRowStagesMax), dev);
+  if (e != cudaSuccess) return e;
+  linear_fp4_rows_kernel<FMT><<<std::min((p.N + 127) / 128, sms), 320, RowCfg::smem(nk), s>>>(m, p);
+  return cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const LinearFp4Params &p, const LinearFp4Maps &m, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  switch (m.form) {
+    case kLinearRows: return launch_rows<FMT>(p, m, dev, sms, s);
+    case kLinearPair: return launch_form<FMT, 2, 256>(p, m, dev, sms, s);
+    case kLinearWide: return launch_form<FMT, 1, 256>(p, m, dev, sms, s);
+    default: return launch_form<FMT, 1, 128>(p, m, dev, sms, s);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_linear_fp4(const LinearFp4Params &p, const LinearFp4Maps &m, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  return m.pair ? launch_form<2, 256>(p, m, sms, s) : launch_form<1, 128>(p, m, sms, s);
+  return p.fmt == kNvfp4 ? launch_fmt<kNvfp4>(p, m, s) : launch_fmt<kMxfp4>(p, m, s);
 }
 
-// The form whose waves over 148 SMs are fewer: a wave of pair tiles takes about as
-// long as one of single tiles.
-bool linear_fp4_pair(int64_t T, int64_t N) {
-  const int64_t pair = ((T + 255) / 256) * ((N + 255) / 256), single = ((T + 127) / 128) * ((N + 127) / 128);
-  return (pair + 73) / 74 < (single + 147) / 148;
+// A few rows of bf16 x are quantised in the product's kernel (kRowItems per thread at most: 1
+// x 18432 x 3072 takes 10.5 us in one launch, 13.4 us in two; at 8 rows of 3072 the
+// quantiser in every CTA would cost 2.5 us more than its own launch). Otherwise the form of
+// the least estimated time on 148 SMs: waves x (time of a tile's ends + time of its
+// K / 256 stages), in units of 10 ns, fitted to measurements of NVFP4 products (us):
+//                            single    wide     pair
+//     333 x 12288 x 3072       13.7    12.6     16.4
+//    1024 x  3072 x 3072       12.2    10.4     10.8
+//    4352 x  9216 x 3072       71.9    66.0     54.6
+//    4352 x  3072 x 12288      86.4    87.9     60.9
+//     512 x  3072 x 12288      18.6    29.2     21.6
+//   10000 x   256 x 256         6.5     6.1      7.1
+LinearFp4Form linear_fp4_form(int64_t T, int64_t N, int64_t K, bool quantised) {
+  const int64_t nk = (K + 255) / 256;
+  if (!quantised && T <= kRowMax && T * nk * 16 <= 256 * kRowItems) return kLinearRows;
+  const int64_t m1 = (T + 127) / 128, m2 = (T + 255) / 256, n1 = (N + 127) / 128, n2 = (N + 255) / 256;
+  const int64_t single = (m1 * n1 + 147) / 148 * (95 + 27 * nk), wide = (m1 * n2 + 147) / 148 * (140 + 50 * nk),
+                pair = 90 + (m2 * n2 + 73) / 74 * (130 + 36 * nk);
+  if (pair < single && pair < wide) return kLinearPair;
+  return wide < single ? kLinearWide : kLinearSingle;
 }
 
 }  // namespace cm

@@ -285,6 +285,14 @@ __device__ __forceinline__ void umma_commit(uint64_t *bar) {
                : "memory");
 }
 
+// ----------------------------------------------------------------- dependent launches
+
+// The kernel launched behind this one with programmatic serialisation may start once every CTA is here.
+__device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// The kernel this one was launched behind is complete and its writes are visible
+// (returns at once after an ordinary launch).
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ----------------------------------------------------------------- CTA pairs (clusters of two)
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -509,12 +517,13 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo_byt
   return d;
 }
 
-// Descriptor of 8-row x 16-byte core matrices laid one after the other, no swizzle.
-__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr) {
+// Descriptor of 8-row x 16-byte core matrices, sbo_bytes from one to the next, no
+// swizzle.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t sbo_bytes) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
   d |= static_cast<uint64_t>(128 >> 4) << 16;
-  d |= static_cast<uint64_t>(128 >> 4) << 32;
+  d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
   d |= static_cast<uint64_t>(1) << 46;
   return d;
 }

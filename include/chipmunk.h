@@ -429,8 +429,10 @@ CHIPMUNK_API chipmunk_status chipmunk_dequantize_fp4_rows(const chipmunk_fp4_row
  *   bias      [N] bf16 or NULL
  *   act       CHIPMUNK_ACT_NONE or CHIPMUNK_ACT_GELU (tanh form)
  *   out       [T][N] of out_type
- * Workspace: chipmunk_workspace_bytes(CHIPMUNK_OP_LINEAR_FP4, a) bytes (the
- * quantised x; none when x is NULL), 16-byte aligned.
+ * Workspace: chipmunk_workspace_bytes(CHIPMUNK_OP_LINEAR_FP4, a) bytes, 16-byte
+ * aligned: the quantised x; none when x is NULL, nor for a few rows (T <= 8 with
+ * T * round_up(K, 256) <= 8192), which the product's kernel
+ * quantises itself, to the same codes.
  */
 #define CHIPMUNK_ACT_NONE 0
 #define CHIPMUNK_ACT_GELU 1

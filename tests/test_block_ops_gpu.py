@@ -184,9 +184,26 @@ def check_linear(cm, rng, T, N, K, fmt, act="none", bias=True, out_dtype=None, q
 @pytest.mark.parametrize("T,N,K", [
     (128, 128, 256), (1, 8, 32), (1, 1024, 512), (130, 136, 288), (2, 4104, 64), (7, 264, 2080), (33, 200, 1056),
     (300, 640, 4128), (129, 128, 16384), (65, 384, 96), (513, 1160, 544),
+    # around the form for a few rows: 8 and 9 rows, its longest rows and the next
+    (8, 136, 96), (9, 136, 96), (8, 264, 1024), (8, 264, 1056), (2, 136, 4096), (1, 128, 8192), (1, 128, 8224), (3, 20000, 256),
 ])
 def test_linear_matches_definition(cm, fmt, T, N, K):
     check_linear(cm, np.random.default_rng(T * 7 + N + K), T, N, K, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T,N,K", [(1, 72, 32), (5, 1000, 544), (8, 4104, 4096), (40, 264, 320), (300, 520, 1056)])
+def test_linear_of_rows_and_of_their_codes_agree(cm, fmt, T, N, K):
+    """Every term is exact and the order of the sums is the tensor core's, so the forms may differ by
+    the rounding of the running sum only; the codes themselves are the same."""
+    import torch
+    rng = np.random.default_rng(T)
+    x = bf16(rows_of(rng, T, K))
+    w = fp4_operand(cm, rng, N, K, fmt)
+    q = cm.quantize_fp4_rows(x, fmt)
+    a, b = (cm.linear_fp4(v, w, out_dtype=torch.float32) for v in (x, q))
+    S = np.abs(f64(cm.dequantize_fp4_rows(q, dtype=torch.float32))) @ np.abs(f64(cm.dequantize_fp4_rows(w, dtype=torch.float32))).T
+    close(f64(a), f64(b), (K / 64 + 8) * 4 * U * S, "rows against codes", stored=2 * U)
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
