@@ -131,17 +131,31 @@ struct RowStats {
   }
 };
 
-// The sample of row t: the last b with offsets[b] <= t, -1 for a row of no sample.
-__device__ __forceinline__ int sample_of(const int32_t *off, int B, int64_t t) {
-  if (t < off[0] || t >= off[B]) return -1;
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (off[mid] <= t) lo = mid;
-    else hi = mid;
+// The sample of a row, the last b with offsets[b] <= row, -1 for a row of no sample. A CTA's
+// rows ascend, so the last answer holds up to the sample's end and costs no loads.
+struct SampleOf {
+  int b = -1;
+  int64_t until = INT64_MIN;  // the answer holds for rows below
+
+  __device__ __forceinline__ int operator()(const int32_t *off, int B, int64_t row) {
+    if (row >= until) {
+      if (row >= off[B]) {
+        b = -1, until = INT64_MAX;
+      } else if (row < off[0]) {
+        b = -1, until = off[0];
+      } else {
+        int lo = 0, hi = B;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (off[mid] <= row) lo = mid;
+          else hi = mid;
+        }
+        b = lo, until = off[hi];
+      }
+    }
+    return b;
   }
-  return lo;
-}
+};
 
 // h = (r * f.x + f.y) * weight + bias, * (1 + scale) + shift, in r.
 template <int NV, bool M32>
@@ -263,12 +277,13 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, ctas_per_sm(W, NV, R32,
       }
     }
   };
+  SampleOf sample;
   int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G;
   fetch(row);
   for (; row < p.T; row += step) {
     int b = 0;
     if (p.offsets != nullptr) {
-      b = sample_of(p.offsets, p.B, row);
+      b = sample(p.offsets, p.B, row);
       if (b < 0) {  // the same for all threads of the row
         fetch(row + step);
         continue;
