@@ -530,12 +530,15 @@ def _here(t, name, dtypes, shape, dev) -> int:
     return t.data_ptr()
 
 
+_DEVICES = [torch.device("cuda", i) for i in range(64)]
+
+
 def _empty(shape, dtype, dev, stream):
     """Uninitialised memory on device ordinal ``dev`` that belongs to the stream that will use it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+        return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+        return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
 
 
 # the current stream's handle without building a Stream object (microseconds, on every call)
@@ -560,18 +563,18 @@ def _call(dev, stream, fn, *args):
         _check(st)
 
 
-def _fp4_scale_bytes(rows, cols, f):
-    return (rows + 127) // 128 * ((cols + 255) // 256) * (2048 if f == NVFP4 else 1024)
-
-
 def _fp4_sizes(rows, cols, fmt):
     """(format, bytes of codes, of block scales, of row scales) of rows x cols 4-bit values, each from a
     256-byte boundary when laid one after the other."""
-    f = _pick(_FP4_FORMATS, fmt, "fmt")
+    f = _FP4_FORMATS.get(fmt)
+    if f is None:
+        f = _pick(_FP4_FORMATS, fmt, "fmt")
     if not 0 <= rows <= 1 << 30 or not 32 <= cols <= 65536 or cols % 32:
         raise ValueError(f"{rows} rows x {cols} columns: columns must be a multiple of 32 in [32, 65536]")
-    return (f, (rows * (cols // 2) + 255) // 256 * 256, _fp4_scale_bytes(rows, cols, f),
-            (rows * 4 + 255) // 256 * 256 if f == NVFP4 else 0)
+    tiles = (rows + 127 >> 7) * (cols + 255 >> 8)
+    if f == NVFP4:
+        return f, (rows * (cols >> 1) + 255) & -256, tiles << 11, (rows * 4 + 255) & -256
+    return f, (rows * (cols >> 1) + 255) & -256, tiles << 10, 0
 
 
 class Fp4Rows:
@@ -604,7 +607,7 @@ class Fp4Rows:
         """Uninitialised rows in one allocation; the tensors over its parts are made when asked for."""
         f, codes, scales, rs = _fp4_sizes(rows, cols, fmt)
         q = cls.__new__(cls)
-        q._buf = _empty((codes + scales + rs,), torch.uint8, dev, stream)
+        q._buf = _empty(codes + scales + rs, torch.uint8, dev, stream)
         q._codes = q._scales = q._row_scales = None
         q.fmt, q.rows, q.cols, q.device_index = fmt, rows, cols, dev
         at = q._buf.data_ptr()
@@ -633,7 +636,7 @@ class Fp4Rows:
 
     @property
     def device(self):
-        return torch.device("cuda", self.device_index)
+        return _DEVICES[self.device_index]
 
 
 def fp4_scale_bytes(rows: int, cols: int, fmt: str) -> int:
@@ -676,8 +679,8 @@ def dequantize_fp4_rows(q: Fp4Rows, out=None, dtype=torch.bfloat16, stream=None)
 
 def linear_fp4_workspace_bytes(T: int, K: int, fmt: str) -> int:
     """Workspace of a linear_fp4 call that quantises its x (none for quantised x, nor for a few rows)."""
-    need = sum(_fp4_sizes(T, K, fmt)[1:])
-    return 0 if T <= 8 and T * ((K + 255) // 256 * 256) <= 8192 else need
+    _, codes, scales, rows = _fp4_sizes(T, K, fmt)
+    return 0 if T <= 8 and T * (K + 255 & -256) <= 8192 else codes + scales + rows
 
 
 def linear_fp4(x, w: Fp4Rows, bias=None, out=None, act="none", out_dtype=torch.bfloat16, workspace=None, stream=None):
@@ -702,7 +705,7 @@ def linear_fp4(x, w: Fp4Rows, bias=None, out=None, act="none", out_dtype=torch.b
         if workspace is None:
             ws_bytes = linear_fp4_workspace_bytes(T, K, w.fmt)
             if ws_bytes:
-                workspace = _empty((ws_bytes,), torch.uint8, dev, stream)
+                workspace = _empty(ws_bytes, torch.uint8, dev, stream)
         else:
             if workspace.get_device() != dev or not workspace.is_contiguous():
                 raise ValueError(f"workspace must be a contiguous tensor on {w.device}")
