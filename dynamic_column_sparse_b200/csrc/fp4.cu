@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) quantize_fp4_rows_kerne
   constexpr int kLanes = FMT == kNvfp4 ? 1 : 2;  // lanes per block
   __shared__ uint32_t row_max[2][16];
   allow_dependents();  // a product launched behind this kernel sets up meanwhile
-  if (*(volatile const int *)p.status != kDevOk) return;
+  if (__syncthreads_or(*(volatile const int *)p.status != kDevOk)) return;  // all threads alike
   const int t = threadIdx.x % G, lane = threadIdx.x & 31;
   const int groups = static_cast<int>(p.cols / 16);
   const int pad_groups = (groups + 15) / 16 * 16;  // whole 256 columns carry scale bytes

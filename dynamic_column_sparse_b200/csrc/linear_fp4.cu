@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(320, 1)
   uint32_t *tmem_slot = row_max + kRowMax;
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (*(volatile int *)p.status != kDevOk) return;
+  if (__syncthreads_or(*(volatile int *)p.status != kDevOk)) return;  // all threads alike
   const int ntiles = (p.N + 127) / 128;
   const int first = blockIdx.x, step = gridDim.x;
 

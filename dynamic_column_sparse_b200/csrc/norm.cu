@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, ctas_per_sm(W, NV, R32,
   constexpr int kRows = (W == 1 ? 128 : G) / G;  // rows a CTA works on at a time
   __shared__ float2 buf[2][16];
   __shared__ float2 cols[16];
-  if (*(volatile const int *)p.status != kDevOk) return;
+  if (__syncthreads_or(*(volatile const int *)p.status != kDevOk)) return;  // all threads alike
   const int t = threadIdx.x % G, warp = t >> 5, lane = t & 31;
   const int D = p.D, ng = D / 8;
   const int nv = t < ng ? (ng - 1 - t) / G + 1 : 0;  // column groups of this thread

@@ -7,6 +7,9 @@ sparse steps in between it recomputes only those columns against the caches
 (Chipmunk blog post, "Activation Deltas Across Diffusion Steps are Very
 Sparse"; the HunyuanVideo table footnote runs 6 of 50 steps denser).
 
+``SparseDeltaBlock`` puts the two layers into the block they belong to, with its
+norms, gates, 4-bit projections (``Fp4Linear``) and head split.
+
 These classes own the device buffers and call the C ABI through
 ``dynamic_column_sparse_b200.chipmunk``; all arithmetic runs in the library's
 CUDA kernels.
@@ -117,6 +120,89 @@ class SparseDeltaAttention:
         else:
             cm.attn_delta(q, k, v, self.idx, self.m_c, self.l_c, self.acc_c, self.o, scale=self.scale, stream=stream)
         return self.o
+
+
+class Fp4Linear:
+    """Dense projection ``act(x W^T + bias)`` with its weight kept as 4-bit microscaled rows.
+
+    ``weight`` [N][K] and ``bias`` [N] bf16 on one CUDA device; the weight is quantised once, here. ``T`` rows at
+    most per call (the scratch for the quantised x is sized for them; calls that run at the same time need
+    an object each)."""
+
+    def __init__(self, weight, bias=None, T: int = 1, fmt: str = "nvfp4", act: str = "none"):
+        self.w = cm.quantize_fp4_rows(weight, fmt)
+        self.bias, self.fmt, self.act = bias, fmt, act
+        self.T = T
+        self.workspace = torch.empty(cm.linear_fp4_workspace_bytes(T, self.w.cols, fmt), dtype=torch.uint8,
+                                     device=weight.device)
+
+    def __call__(self, x, out=None, stream=None):
+        """x: bf16 [t][K], t <= T, or ``Fp4Rows``; out bf16 [t][N]."""
+        if not isinstance(x, cm.Fp4Rows) and x.shape[0] > self.T:
+            raise ValueError(f"{x.shape[0]} rows, the scratch is sized for {self.T}")
+        return cm.linear_fp4(x, self.w, self.bias, out=out, act=self.act, workspace=self.workspace, stream=stream)
+
+
+class SparseDeltaBlock:
+    """A diffusion-transformer block around the two sparse-delta layers, on this library's kernels alone:
+
+        shift1, scale1, gate1, shift2, scale2, gate2 = mod(vec)
+        x += gate1 * proj(attn(heads(qkv(norm(x) * (1 + scale1) + shift1))))
+        x += gate2 * mlp(norm(x) * (1 + scale2) + shift2)
+
+    ``attn`` and ``mlp`` are the block's layers (same T); ``mod`` [6 D][...], ``qkv`` [3 h 128][D] and
+    ``proj`` [D][h 128] are ``Fp4Linear`` of one format, built for 1, T and T rows; ``q_weight``, ``k_weight`` [128]
+    bf16 weigh the norm of the q and k heads. ``refresh`` and ``step`` take x [T][D] (bf16 or fp32, updated
+    in place), the activated conditioning ``vec`` [1][...] bf16 and the rotation's ``cos``, ``sin``
+    [T][64] fp32, and return x, so that ``Schedule.run`` drives a block as it drives a layer."""
+
+    def __init__(self, attn: SparseDeltaAttention, mlp: SparseDeltaMLP, mod: Fp4Linear, qkv: Fp4Linear, proj: Fp4Linear,
+                 q_weight, k_weight, pairs: str = "interleaved", eps: float = 1e-6):
+        T, D, h, dev = attn.T, mlp.D, attn.h, q_weight.device
+        if mlp.T != T:
+            raise ValueError(f"attention is built for {T} tokens, the MLP for {mlp.T}")
+        want = {"mod": (mod, 6 * D, mod.w.cols), "qkv": (qkv, 3 * h * 128, D), "proj": (proj, D, h * 128)}
+        for name, (lin, rows, cols) in want.items():
+            if (lin.w.rows, lin.w.cols) != (rows, cols):
+                raise ValueError(f"{name} has a weight of {lin.w.rows} x {lin.w.cols}, expected {rows} x {cols}")
+        if proj.T < T:
+            raise ValueError(f"proj is built for {proj.T} rows, the block has {T}")
+        self.attn, self.mlp, self.mod, self.qkv, self.proj = attn, mlp, mod, qkv, proj
+        self.q_weight, self.k_weight, self.pairs, self.eps = q_weight, k_weight, pairs, eps
+        self.T, self.D, self.h = T, D, h
+        bf = torch.bfloat16
+        self.m = torch.empty((1, 6 * D), dtype=bf, device=dev)
+        self.h_rows = cm.empty_fp4_rows(T, D, qkv.fmt, dev)
+        self.qkv_out = torch.empty((T, 3 * h * 128), dtype=bf, device=dev)
+        self.q, self.k, self.v = (torch.empty((T, h, 128), dtype=bf, device=dev) for _ in range(3))
+        self.y = torch.empty((T, D), dtype=bf, device=dev)
+        self.h2 = torch.empty((T, D), dtype=bf, device=dev)
+
+    def _run(self, x, vec, cos, sin, dense, stream):
+        D = self.D
+        m = self.mod(vec, out=self.m, stream=stream)
+        shift1, scale1, gate1, shift2, scale2, gate2 = (m[:, i * D:(i + 1) * D] for i in range(6))
+        cm.norm_residual(x, scale=scale1, shift=shift1, eps=self.eps, out=self.h_rows, out_format=self.qkv.fmt,
+                         stream=stream)
+        self.qkv(self.h_rows, out=self.qkv_out, stream=stream)
+        cm.qk_norm_rope(self.qkv_out, self.h, self.q_weight, self.k_weight, cos, sin, pairs=self.pairs, eps=self.eps,
+                        q=self.q, k=self.k, v=self.v, stream=stream)
+        attn = self.attn.refresh if dense else self.attn.step
+        o = attn(self.q, self.k, self.v, stream=stream)
+        self.proj(o.view(self.T, self.h * 128), out=self.y, stream=stream)
+        cm.norm_residual(x, self.y, gate=gate1, res_out=x, scale=scale2, shift=shift2, eps=self.eps, out=self.h2,
+                         stream=stream)
+        mlp = self.mlp.refresh if dense else self.mlp.step
+        cm.norm_residual(x, mlp(self.h2, stream=stream), gate=gate2, res_out=x, out_format=None, stream=stream)
+        return x
+
+    def refresh(self, x, vec, cos, sin, stream=None):
+        """Dense step of both layers; x is updated in place."""
+        return self._run(x, vec, cos, sin, True, stream)
+
+    def step(self, x, vec, cos, sin, stream=None):
+        """Sparse step of both layers; x is updated in place."""
+        return self._run(x, vec, cos, sin, False, stream)
 
 
 class Schedule:

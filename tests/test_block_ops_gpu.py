@@ -422,6 +422,75 @@ def test_heads_from_rows_of_a_wider_tensor(cm):
         assert torch.equal(x, y)
 
 
+# ------------------------------------------------------------------ addresses
+
+def test_tensors_at_16_byte_offsets(cm):
+    """Rows that start 16 bytes into an allocation (the loads and stores of 32 bytes do not apply)."""
+    import torch
+    rng = np.random.default_rng(31)
+    T, C, N = 37, 288, 72
+
+    def shifted(t):
+        flat = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")
+        flat[8:].copy_(t.reshape(-1))
+        return flat[8:].view(t.shape)
+
+    x = bf16(rows_of(rng, T, C))
+    xs = shifted(x)
+    assert xs.data_ptr() % 32 == 16
+    w = fp4_operand(cm, rng, N, C, "nvfp4")
+    for fmt in ("nvfp4", "mxfp4"):
+        a, b = cm.quantize_fp4_rows(x, fmt), cm.quantize_fp4_rows(xs, fmt)
+        assert torch.equal(a.codes, b.codes)
+        va, vb = cm.dequantize_fp4_rows(a), shifted(torch.zeros_like(x))
+        cm.dequantize_fp4_rows(a, out=vb)
+        assert torch.equal(va, vb)
+    for t in (1, T):
+        oa, ob = cm.linear_fp4(x[:t], w), shifted(torch.zeros((t, N), dtype=torch.bfloat16, device="cuda"))
+        cm.linear_fp4(xs[:t], w, out=ob)
+        assert torch.equal(oa, ob)
+    _, ha = cm.norm_residual(x)
+    _, hb = cm.norm_residual(xs, out=shifted(torch.zeros_like(x)))
+    assert torch.equal(ha, hb)
+
+
+def test_tensors_past_31_bit_offsets(cm):
+    """More than 2^31 values: the last rows are what the same rows alone give."""
+    import torch
+    bf = torch.bfloat16
+    T, C = 66000, 32768
+    x = torch.zeros((T, C), dtype=bf, device="cuda")
+    tail = torch.randn(3, C, device="cuda").bfloat16()
+    x[-3:] = tail
+    q = cm.quantize_fp4_rows(x, "nvfp4")
+    del x
+    v = cm.dequantize_fp4_rows(q)
+    assert torch.equal(v[-3:], cm.dequantize_fp4_rows(cm.quantize_fp4_rows(tail, "nvfp4")))
+    del q, v
+    T, D = 132000, 16384
+    x = torch.zeros((T, D), dtype=bf, device="cuda")
+    x[-3:] = tail[:, :D]
+    _, h = cm.norm_residual(x, out=torch.empty_like(x))
+    assert torch.equal(h[-3:], cm.norm_residual(tail[:, :D].contiguous())[1])
+    del x, h
+    T, N = 264000, 8192
+    x = torch.zeros((T, 64), dtype=bf, device="cuda")
+    x[-3:] = tail[:, :64]
+    w = cm.quantize_fp4_rows(torch.randn(N, 64, device="cuda").bfloat16(), "mxfp4")
+    out = cm.linear_fp4(x, w)
+    assert torch.equal(out[-3:], cm.linear_fp4(cm.quantize_fp4_rows(tail[:, :64].contiguous(), "mxfp4"), w))
+    del x, out
+    T, h = 120000, 48
+    qkv = torch.zeros((T, 3 * h * 128), dtype=bf, device="cuda")
+    qkv[-3:] = tail[:, :3 * h * 128]
+    one = torch.ones(128, dtype=bf, device="cuda")
+    ang = torch.rand(T, 64, device="cuda")
+    got = cm.qk_norm_rope(qkv, h, one, one, ang.cos(), ang.sin())
+    want = cm.qk_norm_rope(qkv[-3:].contiguous(), h, one, one, ang.cos()[-3:].contiguous(), ang.sin()[-3:].contiguous())
+    for a, b in zip(got, want):
+        assert torch.equal(a[-3:], b)
+
+
 # ------------------------------------------------------------------ streams, graphs
 
 def test_calls_on_another_stream_and_in_graphs(cm):
@@ -442,6 +511,11 @@ def test_calls_on_another_stream_and_in_graphs(cm):
     got = chain(x, stream=side)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    # both streams at once, each call with memory of its own
+    a = [chain(x, stream=side), chain(x)]
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for got in a for u, v in zip(ref, got))
     # two captured chains, replayed on new inputs
     static = x.clone()
     graphs = []
