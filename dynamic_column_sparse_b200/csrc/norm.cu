@@ -157,10 +157,23 @@ struct SampleOf {
   }
 };
 
-// h = (r * f.x + f.y) * weight + bias, * (1 + scale) + shift, in r.
+// h = (r * f.x + f.y) * weight + bias, * (1 + scale) + shift, in r. The usual case, scale and
+// shift without weight and bias, takes one test.
 template <int NV, bool M32>
 __device__ __forceinline__ void modulate(float (&r)[NV][8], float2 f, const NormParams &p, int nv, int G, int col,
                                          int64_t mod) {
+  const bool plain = p.weight == nullptr && p.bias == nullptr && p.scale != nullptr && p.shift != nullptr;
+  if (plain) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (v < NV - 1 || v < nv) {
+        const Raw8<M32> a = raw8<M32>(p.scale, mod + col + v * G * 8), c = raw8<M32>(p.shift, mod + col + v * G * 8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          r[v][e] = fmaf(fmaf(r[v][e], f.x, f.y), 1.f + at8<M32>(a, e), at8<M32>(c, e));
+      }
+    return;
+  }
 #pragma unroll
   for (int v = 0; v < NV; ++v)
     if (v < NV - 1 || v < nv) {
@@ -229,13 +242,15 @@ __device__ __forceinline__ void write_fp4(const uint4 (&h)[NV], const uint32_t (
   }
 }
 
-// CTAs per SM that the registers are held to (72 to 80 a thread, 128 with four column
-// groups); the grid is one wave of them, so that every CTA walks its rows with the next one
-// in flight. Measured at 20000 rows of 3072 columns: without y four warps of three column groups
-// (53.9 us; with 96 registers 61, with 64 and spills 60), with y six warps of two (81.7 us in bf16, 120 with an
-// fp32 residual; four warps of three 90 and 126).
+// CTAs per SM that the registers are held to (80 a thread, 64 with one column group, 128
+// with four); the grid is one wave of them, so that every CTA walks its rows with the next
+// one in flight. Measured at 20000 rows of 3072 columns: without y four warps of three column groups
+// (45.8 us; with 96 registers 47.8, with 72 and spills 57.7; six warps of two 55.9), with y six warps of
+// two (80.8 us in bf16, 119.5 with an fp32 residual; four warps of three 93 and 139). With y and quantised
+// output four warps of three would take 86.4 instead of 101 us, but the sums' order, and with it
+// some last bits, would then differ between the output formats.
 constexpr int ctas_per_sm(int W, int NV, bool r32, int y) {
-  const int regs = NV == 4 || (NV == 3 && W == 16 && y != 0) ? 128 : NV == 1 ? 64 : y != 0 || r32 ? 80 : NV == 2 ? 64 : 72;
+  const int regs = NV == 4 || (NV == 3 && W == 16 && y != 0) ? 128 : NV == 1 || (NV == 2 && y == 0 && !r32) ? 64 : 80;
   const int n = 65536 / (32 * (W == 1 ? 4 : W) * regs);
   return n < 1 ? 1 : n;
 }
@@ -325,7 +340,13 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, ctas_per_sm(W, NV, R32,
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[v][e] = p.res_scale * at8<R32>(res[v], e);
+        for (int e = 0; e < 8; ++e) r[v][e] = at8<R32>(res[v], e);
+      if (p.res_scale != 1.f) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[v][e] *= p.res_scale;
+      }
     }
     fetch(row + step);
     if (p.res_out != nullptr) {

@@ -329,7 +329,7 @@ def test_norm_packed_samples(cm, offsets, D):
     check_norm(cm, rng, 40, D, "layer", "rms", B=len(offsets) - 1, offsets=offsets)
 
 
-@pytest.mark.parametrize("D", [32, 64, 288, 1056, 3072, 5152, 16384])
+@pytest.mark.parametrize("D", [32, 64, 288, 1056, 1504, 3072, 5152, 8192, 10016, 16384])
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4", "e4m3"])
 def test_norm_quantised_output_equals_the_quantiser(cm, D, fmt):
     """The quantised rows are those of the bf16 output, byte for byte."""
