@@ -496,10 +496,7 @@ def _pick(table, key, name):
         raise ValueError(f"{name} must be one of {', '.join(map(str, table))}, got {key!r}") from None
 
 
-_BF16 = (torch.bfloat16,)
-_F32 = (torch.float32,)
-_U8 = (torch.uint8,)
-_I32 = (torch.int32,)
+_BF16, _F32, _U8, _I32 = ((t,) for t in (torch.bfloat16, torch.float32, torch.uint8, torch.int32))
 _BF16_F32 = (torch.bfloat16, torch.float32)
 
 
@@ -517,6 +514,9 @@ def _device_of(t, name, dtypes) -> int:
 
 def _here(t, name, dtypes, shape, dev) -> int:
     """Address of a contiguous tensor of one of ``dtypes`` and of ``shape`` on device ordinal ``dev``."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == dev and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
@@ -525,9 +525,7 @@ def _here(t, name, dtypes, shape, dev) -> int:
         raise ValueError(f"{name} must be on CUDA device {dev}, is on {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 _DEVICES = [torch.device("cuda", i) for i in range(64)]
@@ -544,6 +542,7 @@ def _empty(shape, dtype, dev, stream):
 # the current stream's handle without building a Stream object (microseconds, on every call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(dev, stream, fn, *args):
@@ -554,7 +553,7 @@ def _call(dev, stream, fn, *args):
         raise ValueError(f"stream is on {stream.device}, the tensors on CUDA device {dev}")
     else:
         handle = stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -654,7 +653,7 @@ def empty_fp4_rows(rows: int, cols: int, fmt: str, device, stream=None) -> Fp4Ro
 
 def quantize_fp4_rows(x, fmt="nvfp4", out: Fp4Rows | None = None, stream=None) -> Fp4Rows:
     """Rows of bf16 x [R][C] to 4-bit microscaled rows (C a multiple of 32)."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = _device_of(x, "x", _BF16)
     R, C = x.shape
     px = _here(x, "x", _BF16, (R, C), dev)
@@ -668,7 +667,7 @@ def quantize_fp4_rows(x, fmt="nvfp4", out: Fp4Rows | None = None, stream=None) -
 
 def dequantize_fp4_rows(q: Fp4Rows, out=None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """The values that 4-bit rows stand for, [R][C] in bf16 (exact) or fp32."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = q.device_index
     if out is None:
         out = _empty((q.rows, q.cols), dtype, dev, stream)
@@ -687,7 +686,7 @@ def linear_fp4(x, w: Fp4Rows, bias=None, out=None, act="none", out_dtype=torch.b
     """act(x w^T + bias) on 4-bit operands: x bf16 [T][K] (quantised inside, into ``workspace``) or
     Fp4Rows [T][K], w Fp4Rows [N][K], bias bf16 [N], out [T][N] bf16 or fp32. Calls that run at
     the same time, captured ones included, must not share a workspace."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev, N, K = w.device_index, w.rows, w.cols
     px = pw = None
     ws_bytes = 0
@@ -720,6 +719,18 @@ def linear_fp4(x, w: Fp4Rows, bias=None, out=None, act="none", out_dtype=torch.b
     return out
 
 
+def _mod_row(t, name, dtype, shape, ld, dev) -> int:
+    """Address of a gate, scale or shift [B][D] of the others' type and row stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError("gate, scale and shift must be tensors of one type, bfloat16 or float32")
+    if t.get_device() != dev or t.shape != shape or t.stride(1) != 1:
+        raise ValueError(f"{name} must be {list(shape)} on CUDA device {dev} with consecutive columns, "
+                         f"is {list(t.shape)} on {t.device}")
+    if shape[0] > 1 and t.stride(0) != ld:
+        raise ValueError("gate, scale and shift must have the same row stride")
+    return t.data_ptr()
+
+
 def norm_residual(res, y=None, *, gate=None, post_norm="none", post_weight=None, res_scale=1.0, res_out=None,
                   norm="layer", weight=None, bias=None, scale=None, shift=None, offsets=None, eps=1e-6, out=None,
                   out_format="bf16", stream=None):
@@ -730,7 +741,7 @@ def norm_residual(res, y=None, *, gate=None, post_norm="none", post_weight=None,
     None for one sample. Returns (res_out, h): res_out is written when it is given (``res`` itself
     updates in place) or when y is; h is bf16, (e4m3 codes, row scales) or Fp4Rows as out_format
     says, into ``out`` when given, or None for out_format=None."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = _device_of(res, "res", _BF16_F32)
     shape = res.shape
     T, D = shape
@@ -751,21 +762,17 @@ def norm_residual(res, y=None, *, gate=None, post_norm="none", post_weight=None,
         if B < 1:
             raise ValueError("offsets must hold at least two values")
         p_off = _here(offsets, "offsets", _I32, (B + 1,), dev)
-    mod_type = ld = None
-    mods = []
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if t is None:
-            mods.append(None)
-            continue
-        if not isinstance(t, torch.Tensor) or t.dtype not in _BF16_F32 or t.dtype != (mod_type or t.dtype):
-            raise TypeError("gate, scale and shift must be tensors of one type, bfloat16 or float32")
-        if t.get_device() != dev or t.shape != (B, D) or t.stride(1) != 1:
-            raise ValueError(f"{name} must be [{B}][{D}] on {res.device} with consecutive columns, is {tuple(t.shape)} on {t.device}")
-        row = t.stride(0) if B > 1 else D
-        if ld is not None and row != ld:
-            raise ValueError("gate, scale and shift must have the same row stride")
-        mod_type, ld = t.dtype, row
-        mods.append(t.data_ptr())
+    first = gate if gate is not None else scale if scale is not None else shift
+    p_gate = p_scale = p_shift = None
+    mod_type = ld = 0
+    if first is not None:
+        if not isinstance(first, torch.Tensor) or first.dtype not in _BF16_F32 or first.dim() != 2:
+            raise TypeError("gate, scale and shift must be 2-D tensors of one type, bfloat16 or float32")
+        mod_type, ld = _TYPES[first.dtype], first.stride(0) if B > 1 else D
+        like = (first.dtype, (B, D), ld, dev)
+        p_gate = None if gate is None else _mod_row(gate, "gate", *like)
+        p_scale = None if scale is None else _mod_row(scale, "scale", *like)
+        p_shift = None if shift is None else _mod_row(shift, "shift", *like)
     h, f = None, 0
     if out_format is not None:
         f = _pick(_NORM_OUT, out_format, "out_format")
@@ -783,9 +790,9 @@ def norm_residual(res, y=None, *, gate=None, post_norm="none", post_weight=None,
             if not isinstance(h, Fp4Rows) or (h.rows, h.cols, h.fmt, h.device_index) != (T, D, out_format, dev):
                 raise ValueError(f"out must be Fp4Rows of {T} x {D} {out_format} on {res.device}")
             p_out, p_sc, p_rs = h.args.codes, h.args.scales, h.args.row_scales
-    a = NormArgs(T, D, B, _TYPES[res.dtype], y_type, 0 if mod_type is None else _TYPES[mod_type],
-                 _pick(_NORMS, post_norm, "post_norm"), _pick(_NORMS, norm, "norm"), f, eps, res_scale, p_res, p_y, p_pw,
-                 mods[0], p_ro, p_w, p_b, mods[1], mods[2], ld or 0, p_off, p_out, p_sc, p_rs)
+    a = NormArgs(T, D, B, _TYPES[res.dtype], y_type, mod_type, _pick(_NORMS, post_norm, "post_norm"),
+                 _pick(_NORMS, norm, "norm"), f, eps, res_scale, p_res, p_y, p_pw, p_gate, p_ro, p_w, p_b, p_scale, p_shift,
+                 ld, p_off, p_out, p_sc, p_rs)
     _call(dev, stream, lib.chipmunk_norm_residual, a)
     return res_out, h
 
@@ -795,7 +802,7 @@ def qk_norm_rope(qkv, h, q_weight, k_weight, cos, sin, pairs="interleaved", eps=
     """Heads out of a fused projection: qkv bf16 [T][>= 3 h 128] (rows may be strided), RMS norm of each
     q and k head with q_weight, k_weight bf16 [128], rotation by cos, sin fp32 [T][64]; returns q, k,
     v bf16 [T][h][128]."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = _device_of(qkv, "qkv", _BF16)
     T, C = qkv.shape
     if qkv.stride(1) != 1 or C < 3 * h * 128:

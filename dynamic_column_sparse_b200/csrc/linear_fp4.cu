@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(320, 1)
   const bool run = (CG == 2 ? cluster_load(cluster_addr(go, 0)) : *go) != 0;
 
   if (!run) {
+    wait_for_primary();  // this kernel is complete only when the one before it is
   } else if (warp == 0) {
     const uint32_t lead = elect_lane();
     // loads of stage kg (K block kb of a tile) into slot s: w's, or x's
