@@ -265,17 +265,9 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, ctas_per_sm(W, NV, R32,
   constexpr int kRows = (W == 1 ? 128 : G) / G;  // rows a CTA works on at a time
   __shared__ float2 buf[2][16];
   __shared__ float2 cols[16];
-  if (__syncthreads_or(*(volatile const int *)p.status != kDevOk)) return;  // all threads alike
   const int t = threadIdx.x % G, warp = t >> 5, lane = t & 31;
   const int D = p.D, ng = D / 8;
   const int nv = t < ng ? (ng - 1 - t) / G + 1 : 0;  // column groups of this thread
-  if (threadIdx.x < W) {
-    int n = 0;
-    for (int v = 0; v < NV; ++v) n += min(max(ng - v * G - static_cast<int>(threadIdx.x) * 32, 0), 32);
-    cols[threadIdx.x] = make_float2(8.f * n, n > 0 ? 1.f / (8.f * n) : 0.f);
-  }
-  __syncthreads();
-  RowStats<W, NV> st{buf, cols, 1.f / static_cast<float>(D), p.eps, nv, warp, lane};
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   // The next row's loads go out as soon as this row's inputs are used up, before its last
   // norm: registers hold one row of inputs in flight per thread.
@@ -292,9 +284,16 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, ctas_per_sm(W, NV, R32,
       }
     }
   };
-  SampleOf sample;
   int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G;
   fetch(row);
+  if (threadIdx.x < W) {
+    int n = 0;
+    for (int v = 0; v < NV; ++v) n += min(max(ng - v * G - static_cast<int>(threadIdx.x) * 32, 0), 32);
+    cols[threadIdx.x] = make_float2(8.f * n, n > 0 ? 1.f / (8.f * n) : 0.f);
+  }
+  if (__syncthreads_or(*(volatile const int *)p.status != kDevOk)) return;  // all threads alike
+  RowStats<W, NV> st{buf, cols, 1.f / static_cast<float>(D), p.eps, nv, warp, lane};
+  SampleOf sample;
   for (; row < p.T; row += step) {
     int b = 0;
     if (p.offsets != nullptr) {
