@@ -532,11 +532,12 @@ _DEVICES = [torch.device("cuda", i) for i in range(64)]
 
 
 def _empty(shape, dtype, dev, stream):
-    """Uninitialised memory on device ordinal ``dev`` that belongs to the stream that will use it."""
+    """Uninitialised memory on device ordinal ``dev`` that belongs to the stream that will use it. (Sizes one by
+    one: a tuple of them costs torch.empty almost a microsecond more.)"""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
+        return torch.empty(*shape, dtype=dtype, device=_DEVICES[dev])
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
+        return torch.empty(*shape, dtype=dtype, device=_DEVICES[dev])
 
 
 # the current stream's handle without building a Stream object (microseconds, on every call)
@@ -606,7 +607,7 @@ class Fp4Rows:
         """Uninitialised rows in one allocation; the tensors over its parts are made when asked for."""
         f, codes, scales, rs = _fp4_sizes(rows, cols, fmt)
         q = cls.__new__(cls)
-        q._buf = _empty(codes + scales + rs, torch.uint8, dev, stream)
+        q._buf = _empty((codes + scales + rs,), torch.uint8, dev, stream)
         q._codes = q._scales = q._row_scales = None
         q.fmt, q.rows, q.cols, q.device_index = fmt, rows, cols, dev
         at = q._buf.data_ptr()
@@ -704,7 +705,7 @@ def linear_fp4(x, w: Fp4Rows, bias=None, out=None, act="none", out_dtype=torch.b
         if workspace is None:
             ws_bytes = linear_fp4_workspace_bytes(T, K, w.fmt)
             if ws_bytes:
-                workspace = _empty(ws_bytes, torch.uint8, dev, stream)
+                workspace = _empty((ws_bytes,), torch.uint8, dev, stream)
         else:
             if workspace.get_device() != dev or not workspace.is_contiguous():
                 raise ValueError(f"workspace must be a contiguous tensor on {w.device}")
