@@ -11,14 +11,17 @@
 //
 // Warp 0 fills a ring of stages of 256 columns with TMA: code tiles
 // (128-byte swizzle) and the block scales' 512-byte tiles. Warp 1 (of the leading CTA)
-// copies scales to TMEM and issues the MMAs. The scale columns are a ring of
-// their own, one slot per scale tile, filled one slot ahead of the MMAs: with a
-// copy and its MMAs back to back the tensor core idled more than half the time
-// (546 of 1240 cycles per stage busy, ncu). Warps 2-9 drain one accumulator (scales,
-// bias, activation, rounding, TMA stores through swizzled shared memory) while
+// copies scales to TMEM and issues the MMAs. What bounded it first was the issuing: inside a
+// one-lane branch every tcgen05 instruction took 100 to 150 cycles, against about 21 for a
+// scale copy and 33 for an MMA when the whole warp computes the operands and the elected lane is the
+// instruction's predicate (4352 x 9216 x 3072: 149.8 -> 70.6 us). The scale columns are a ring of
+// their own, one slot per scale tile, filled one slot ahead of the MMAs. Warps 2-9 drain one
+// accumulator (scales, bias, activation, rounding, TMA stores through swizzled shared memory) while
 // the other is being filled. At 256 columns the two accumulators share 64 TMEM
 // columns, which leaves 64 for the scales: the shared columns are drained first and the next
-// tile's MMAs wait for them only.
+// tile's MMAs wait for them only (about 800 cycles of the 6900 that a tile with K = 3072 takes).
+// With K = 12288 the MMAs are issued every 544 cycles per stage, 512 being the tensor pipe's; in
+// a sustained run the power cap bounds the product.
 #include <algorithm>
 #include <atomic>
 
@@ -661,9 +664,10 @@ cudaError_t launch_linear_fp4(const LinearFp4Params &p, const LinearFp4Maps &m, 
   return p.fmt == kNvfp4 ? launch_fmt<kNvfp4>(p, m, s) : launch_fmt<kMxfp4>(p, m, s);
 }
 
-// A few rows of bf16 x are quantised in the product's kernel (kRowItems per thread at most: 1
-// x 18432 x 3072 takes 10.5 us in one launch, 13.4 us in two; at 8 rows of 3072 the
-// quantiser in every CTA would cost 2.5 us more than its own launch). Otherwise the form of
+// A few rows of bf16 x are quantised in the product's kernel (kRowItems per thread at most): 1
+// x 18432 x 3072 takes 10.5 us in one launch, 12.9 us in two, 1 x 3072 x 3072 9.1 against 8.6 us, and a
+// call costs the host 5 us less; at 8 rows of 3072 the quantiser in every CTA would take 2.5 us
+// more than its own launch. Otherwise the form of
 // the least estimated time on 148 SMs: waves x (time of a tile's ends + time of its
 // K / 256 stages), in units of 10 ns, fitted to measurements of NVFP4 products (us):
 //                            single    wide     pair

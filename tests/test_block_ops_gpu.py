@@ -186,6 +186,9 @@ def check_linear(cm, rng, T, N, K, fmt, act="none", bias=True, out_dtype=None, q
     (300, 640, 4128), (129, 128, 16384), (65, 384, 96), (513, 1160, 544),
     # around the form for a few rows: 8 and 9 rows, its longest rows and the next
     (8, 136, 96), (9, 136, 96), (8, 264, 1024), (8, 264, 1056), (2, 136, 4096), (1, 128, 8192), (1, 128, 8224), (3, 20000, 256),
+    # few rows against few and many weight rows, short and long sums
+    (1, 3072, 3072), (8, 3072, 3072), (5, 512, 1824), (8, 1000, 4096), (1, 256, 65536), (2, 200, 32768), (1, 9216, 1056),
+    (8, 128, 16384), (1, 64, 1536), (7, 1160, 12288), (4, 6000, 2048),
 ])
 def test_linear_matches_definition(cm, fmt, T, N, K):
     check_linear(cm, np.random.default_rng(T * 7 + N + K), T, N, K, fmt)
