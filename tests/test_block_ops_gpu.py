@@ -535,3 +535,79 @@ def test_calls_on_another_stream_and_in_graphs(cm):
             g.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(want, outs))
+
+
+# ------------------------------------------------------------------ refusals and the status word
+
+def test_refusals_of_device_tensors(cm):
+    import torch
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device="cuda")
+    w = cm.quantize_fp4_rows(z(72, 64) + 1)
+    with pytest.raises(cm.ChipmunkError, match="T=0"):
+        cm.linear_fp4(z(0, 64), w)
+    with pytest.raises(cm.ChipmunkError, match="T=0"):
+        cm.norm_residual(z(0, 64))
+    with pytest.raises(cm.ChipmunkError, match="N=12"):
+        cm.linear_fp4(z(3, 64), cm.quantize_fp4_rows(z(12, 64)))
+    with pytest.raises(cm.ChipmunkError, match="D=12"):
+        cm.norm_residual(z(3, 12))
+    with pytest.raises(cm.ChipmunkError, match="need y"):
+        cm.norm_residual(z(3, 64), gate=z(1, 64))
+    with pytest.raises(cm.ChipmunkError, match="ld_mod"):
+        cm.norm_residual(z(3, 64), scale=z(1, 64).expand(2, 64), offsets=torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda"))
+    with pytest.raises(cm.ChipmunkError) as e:
+        cm.linear_fp4(z(30, 64), w, workspace=z(16, dtype=torch.uint8))
+    assert e.value.status == cm.ERR_WORKSPACE
+    with pytest.raises(ValueError, match="contiguous"):
+        cm.linear_fp4(z(64, 3).t(), w)
+    with pytest.raises(ValueError, match="columns"):
+        cm.linear_fp4(cm.quantize_fp4_rows(z(3, 64), "mxfp4"), w)
+    with pytest.raises(ValueError, match="x must|shape"):
+        cm.linear_fp4(z(3, 96), w)
+    with pytest.raises(TypeError, match="one type"):
+        cm.norm_residual(z(3, 64), scale=z(1, 64, dtype=torch.float32), shift=z(1, 64))
+    with pytest.raises(ValueError, match="scale must be"):
+        cm.norm_residual(z(3, 64), scale=z(2, 64))
+    with pytest.raises(ValueError, match="multiple of 32"):
+        cm.quantize_fp4_rows(z(3, 48))
+    with pytest.raises(ValueError, match="384"):
+        cm.qk_norm_rope(z(3, 100), 1, z(128), z(128), z(3, 64), z(3, 64))
+    # no rows: nothing to quantise, and nothing comes back
+    q = cm.quantize_fp4_rows(z(0, 64))
+    assert q.rows == 0 and cm.dequantize_fp4_rows(q).shape == (0, 64)
+
+
+def test_calls_are_skipped_while_the_status_word_is_set(cm):
+    """A wait that ran out elsewhere: every later kernel returns without touching its outputs, the product's
+    CTA pairs and the kernel launched behind a skipped quantiser included; cleared, all run again."""
+    import torch
+    rng = np.random.default_rng(40)
+    sizes = [(1, 128, 96), (300, 264, 512), (2560, 2304, 512)]        # a few rows, single tiles, pairs
+    ops = []
+    for T, N, K in sizes:
+        x, w = bf16(rows_of(rng, T, K)), fp4_operand(cm, rng, N, K, "nvfp4")
+        out = torch.full((T, N), 3.0, dtype=torch.bfloat16, device="cuda")
+        ops.append((out, lambda x=x, w=w, out=out: cm.linear_fp4(x, w, out=out)))
+    x = bf16(rows_of(rng, 40, 512))
+    h = torch.full_like(x, 3.0)
+    ops.append((h, lambda: cm.norm_residual(x, out=h)))
+    q, d = cm.quantize_fp4_rows(x), torch.full_like(x, 3.0)
+    ops.append((d, lambda: cm.dequantize_fp4_rows(q, out=d)))
+    q2 = cm.empty_fp4_rows(40, 512, "mxfp4", "cuda")
+    q2.codes.fill_(3)
+    ops.append((q2.codes, lambda: cm.quantize_fp4_rows(x, "mxfp4", out=q2)))
+    hd = [torch.full((8, 1, 128), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    qkv, hw, ang = bf16(rng.standard_normal((8, 384))), bf16(np.ones(128)), f32(np.zeros((8, 64)))
+    ops.append((hd[2], lambda: cm.qk_norm_rope(qkv, 1, hw, hw, ang, ang, q=hd[0], k=hd[1], v=hd[2])))
+    lib = cm.load_library()
+    assert lib.chipmunk_selftest_bounded_wait(torch.cuda.current_stream().cuda_stream) == 0
+    for out, call in ops:
+        call()
+    torch.cuda.synchronize()
+    for out, _ in ops:
+        assert bool((out == 3).all())
+    assert cm.read_device_status() == 1
+    for out, call in ops:
+        call()
+    torch.cuda.synchronize()
+    assert all(not bool((out == 3).all()) for out, _ in ops)
