@@ -43,7 +43,7 @@ EXPORTS = (
     "chipmunk_last_error", "chipmunk_read_device_status", "chipmunk_version", "chipmunk_mlp_delta_noalloc",
     "chipmunk_selftest_bounded_wait", "chipmunk_mlp_delta_fp8", "chipmunk_quantize_e4m3_rows",
     "chipmunk_fp4_scale_bytes", "chipmunk_quantize_fp4_rows", "chipmunk_dequantize_fp4_rows", "chipmunk_linear_fp4",
-    "chipmunk_norm_residual", "chipmunk_qk_norm_rope",
+    "chipmunk_norm_residual", "chipmunk_qk_norm_rope", "chipmunk_selftest_linear_fp4_form",
 )
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -162,6 +162,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "chipmunk_linear_fp4": [ctypes.POINTER(LinearFp4Args), vp, sz, vp],
             "chipmunk_norm_residual": [ctypes.POINTER(NormArgs), vp],
             "chipmunk_qk_norm_rope": [ctypes.POINTER(HeadsArgs), vp],
+            "chipmunk_selftest_linear_fp4_form": [i64, i64, i64, i32],
         }
         for name, argtypes in sig.items():
             fn = getattr(lib, name)

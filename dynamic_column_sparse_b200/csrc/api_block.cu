@@ -42,12 +42,15 @@ chipmunk_status check_ptrs(const Ptr *ptrs, int n) {
   return CHIPMUNK_OK;
 }
 
-constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxN = int64_t(1) << 20;
 
 bool fp4_sizes_ok(int64_t rows, int64_t cols, int32_t format) {
   return rows >= 0 && rows <= kMaxRows && cols >= 32 && cols <= 65536 && cols % 32 == 0 &&
          (format == CHIPMUNK_NVFP4 || format == CHIPMUNK_MXFP4);
 }
+
+// The product's tiles are counted in 31 bits.
+bool linear_tiles_ok(int64_t T, int64_t N) { return ((T + 127) / 128) * ((N + 127) / 128) < (int64_t(1) << 31); }
 
 chipmunk_status check_fp4(const chipmunk_fp4_rows *q, const char *what) {
   if (q == nullptr) return record_errorf(CHIPMUNK_ERR_INVALID_ARG, "%s is NULL", what);
@@ -161,9 +164,9 @@ chipmunk_status chipmunk_linear_fp4(const chipmunk_linear_fp4_args *a, void *ws,
                                     chipmunk_stream stream) {
   if (a == nullptr) return record_errorf(CHIPMUNK_ERR_INVALID_ARG, "args is NULL");
   if (a->T < 1 || a->T > kMaxRows) return record_errorf(CHIPMUNK_ERR_SHAPE, "T=%lld out of range", (long long)a->T);
-  if (a->N < 8 || a->N > (int64_t(1) << 20) || a->N % 8 != 0)
+  if (a->N < 8 || a->N > kMaxN || a->N % 8 != 0)
     return record_errorf(CHIPMUNK_ERR_SHAPE, "N=%lld must be a multiple of 8 in [8, 2^20]", (long long)a->N);
-  if (((a->T + 127) / 128) * ((a->N + 127) / 128) >= (int64_t(1) << 31))
+  if (!linear_tiles_ok(a->T, a->N))
     return record_errorf(CHIPMUNK_ERR_SHAPE, "T=%lld x N=%lld is too large", (long long)a->T, (long long)a->N);
   if (a->act != CHIPMUNK_ACT_NONE && a->act != CHIPMUNK_ACT_GELU)
     return record_errorf(CHIPMUNK_ERR_INVALID_ARG, "act %d unknown", a->act);
@@ -214,6 +217,11 @@ chipmunk_status chipmunk_linear_fp4(const chipmunk_linear_fp4_args *a, void *ws,
                         status};
   CM_CUDA(cm::launch_linear_fp4(p, m, s), "4-bit linear launch");
   return CHIPMUNK_OK;
+}
+
+int32_t chipmunk_selftest_linear_fp4_form(int64_t T, int64_t N, int64_t K, int32_t quantised) {
+  if (T < 1 || N < 8 || N > kMaxN || N % 8 != 0 || !fp4_sizes_ok(T, K, CHIPMUNK_NVFP4) || !linear_tiles_ok(T, N)) return -1;
+  return cm::linear_fp4_form(T, N, K, quantised != 0);
 }
 
 chipmunk_status chipmunk_norm_residual(const chipmunk_norm_args *a, chipmunk_stream stream) {

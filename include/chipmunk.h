@@ -557,6 +557,14 @@ CHIPMUNK_API chipmunk_status chipmunk_read_device_status(int32_t *host_out, chip
  */
 CHIPMUNK_API chipmunk_status chipmunk_selftest_bounded_wait(chipmunk_stream stream);
 
+/*
+ * Diagnostic for tests: the form of the kernel that chipmunk_linear_fp4 takes for a
+ * T x N x K product (quantised: x comes as 4-bit rows): 0 a few rows, 1 128 x 128 tiles,
+ * 2 CTA pairs on 256 x 256 tiles, 3 128 x 256 tiles; -1 for sizes that the call refuses.
+ * Touches no device.
+ */
+CHIPMUNK_API int32_t chipmunk_selftest_linear_fp4_form(int64_t T, int64_t N, int64_t K, int32_t quantised);
+
 /* Library version, e.g. "0.1.0". */
 CHIPMUNK_API const char *chipmunk_version(void);
 
