@@ -581,8 +581,9 @@ def _fp4_sizes(rows, cols, fmt):
 class Fp4Rows:
     """Rows of 4-bit microscaled values: ``codes`` uint8 [rows][cols / 2] (lower column in the low
     nibble), ``scales`` uint8 (block scales in the tensor core's order, ``fp4_scale_bytes`` of
-    them), ``row_scales`` fp32 [rows] (nvfp4; None for mxfp4). The header of the C ABI defines both
-    formats and the order of the scales."""
+    them), ``row_scales`` fp32 [rows] (nvfp4; None for mxfp4): powers of two out of ``quantize_fp4_rows``, any
+    scale from 2^-110 to 2^117 in rows made elsewhere (a tensor's one scale, repeated). The header of
+    the C ABI defines both formats and the order of the block scales."""
 
     __slots__ = ("_codes", "_scales", "_row_scales", "_buf", "fmt", "rows", "cols", "device_index", "args")
 

@@ -44,7 +44,9 @@ struct LinCfg {
   static constexpr uint32_t kOutBytes = 4096;  // 32 rows x 128 bytes, one per epilogue warp
   static constexpr uint32_t kOutOff = kStages * kStageBytes;
   static constexpr uint32_t kColOff = kOutOff + 8 * kOutBytes;  // [BN] row scale of w and bias, bf16 each
-  static constexpr uint32_t kBarOff = kColOff + BN * 4;
+  static constexpr uint32_t kRatioOff = kColOff + BN * 4;       // [BN] row scale of w over its bf16
+  static constexpr uint32_t kFlagOff = kRatioOff + BN * 4;      // [8] does a warp's part of the columns have other ratios than 1
+  static constexpr uint32_t kBarOff = kFlagOff + 32;
   static constexpr uint32_t kSmem = 1024 + kBarOff + 256;
   static constexpr uint32_t kAcc1 = BN == 256 ? 192 : BN;        // TMEM column of the second accumulator
   static constexpr uint32_t kSfCol = kAcc1 + BN;                 // scale slots: 4 columns of x, BN / 32 of w
@@ -249,6 +251,8 @@ __global__ void __launch_bounds__(320, 1)
     const int e = threadIdx.x - 64;
     uint8_t *stage = smem + C::kOutOff + (warp - 2) * C::kOutBytes;
     uint32_t *cols = reinterpret_cast<uint32_t *>(smem + C::kColOff);
+    float *ratios = reinterpret_cast<float *>(smem + C::kRatioOff);
+    uint32_t *flags = reinterpret_cast<uint32_t *>(smem + C::kFlagOff);
     int tl = 0;
     wait_for_primary();  // the row scales of x
     // a drained accumulator (or its shared columns) goes back to the leader's MMA warp
@@ -266,21 +270,38 @@ __global__ void __launch_bounds__(320, 1)
       const int mt = tile / tiles_n, nt = tile - mt * tiles_n;
       const int ab = tl & 1;
       const int row0 = (mt * CG + rank) * 128 + quad * 32;
-      // this row's factor; this thread's column: row scale of w above, bias below, both bf16
+      // this row's factor; this thread's column: row scale of w above, bias below, both bf16, which holds
+      // the quantiser's powers of two and NaN; for other scales a ratio makes up for it
       const float rx = S16 && row0 + lane < p.T ? p.rx[row0 + lane] : 1.f;
       const int n = nt * BN + e;
+      float ratio = 1.f;
       uint32_t col = 0x3f800000u;
       if (e < BN && n < p.N) {
-        if (S16) col = static_cast<uint32_t>(f32_to_bf16_bits(p.rw[n])) << 16;
+        if (S16) {
+          const float rw = p.rw[n];
+          const uint32_t hi = f32_to_bf16_bits(rw);
+          col = hi << 16;
+          if ((__float_as_uint(rw) & 0xffffu) != 0) ratio = __fdiv_rn(rw, bf16_lo(hi));
+        }
         if (p.bias != nullptr) col |= p.bias[n];
       }
+      const bool odd = S16 && __any_sync(0xffffffffu, ratio != 1.f);
       // the warps have read the previous tile's column values; put this tile's in place
       if (lane == 0) mbar_arrive(col_bar);
       if (!wait_warp(col_bar, 0, p.status, abort_flag)) break;
-      if (e < BN) cols[e] = col;
+      if (e < BN) {
+        cols[e] = col;
+        if (S16) ratios[e] = ratio;
+      }
+      if (S16 && lane == 0) flags[warp - 2] = odd;
       __syncwarp();
       if (lane == 0) mbar_arrive(col_bar);
       if (!wait_warp(col_bar, 1, p.status, abort_flag)) break;
+      bool odd_scales = false;  // the same for all warps
+      if (S16) {
+        const uint4 f0 = reinterpret_cast<const uint4 *>(flags)[0], f1 = reinterpret_cast<const uint4 *>(flags)[1];
+        odd_scales = (f0.x | f0.y | f0.z | f0.w | f1.x | f1.y | f1.z | f1.w) != 0;
+      }
       if (!wait_warp(&acc_full[ab], (tl >> 1) & 1, p.status, abort_flag)) break;
       tc_fence_after();
       // The columns both accumulators share are the last 64 of the first one and the
@@ -292,6 +313,16 @@ __global__ void __launch_bounds__(320, 1)
         tmem_ld64(tmem + ab * C::kAcc1 + (static_cast<uint32_t>(quad * 32) << 16) + c0, v);
         if (has_shared && i == 0) release(shared_empty);
         if (i == kChunks - 1) release(&acc_empty[ab]);
+        // The part of w's row scales that the bf16 below does not hold: two roundings more (ratio and product), in
+        // tiles with such scales only, where it takes 79 instead of 64 us at 12000 x 9216 x 256, 51 instead of
+        // 46 at 4352 x 12288 x 1024, and is hidden behind the MMAs at longer sums.
+        if (S16 && odd_scales) {
+#pragma unroll
+          for (int q = 0; q < 64; q += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(ratios + c0 + q);
+            v[q] *= f.x, v[q + 1] *= f.y, v[q + 2] *= f.z, v[q + 3] *= f.w;
+          }
+        }
         // Every lane reads every column's values, a shared-memory wavefront for each
         // word: with fp32 values these reads were the longest part of the epilogue.
 #pragma unroll
@@ -384,7 +415,7 @@ struct RowCfg {
   static constexpr uint32_t kXBytes = 1024, kSxBytes = 512;  // x per 256 columns: codes; scales, 128 bytes per tile
   static constexpr uint32_t kXOff = kStages * kStageBytes;
   static constexpr uint32_t kBarBytes = 512;
-  static constexpr uint32_t smem(int nk) { return 1024 + kXOff + nk * (kXBytes + kSxBytes) + 2 * 128 * 4 + kBarBytes; }
+  static constexpr uint32_t smem(int nk) { return 1024 + kXOff + nk * (kXBytes + kSxBytes) + 2 * 128 * 8 + kBarBytes; }
   static constexpr uint32_t kSfCol = 256, kSfCols = 8;
   static constexpr int kSfSlots = 5;
 };
@@ -402,7 +433,7 @@ __global__ void __launch_bounds__(320, 1)
   const int nk = (p.K + 255) / 256;
   uint8_t *xs = smem + C::kXOff;                    // codes, 1 KB per 256 columns
   uint8_t *sx = xs + nk * C::kXBytes;               // scales, 128 bytes per scale tile
-  uint32_t *cols = reinterpret_cast<uint32_t *>(sx + nk * C::kSxBytes);  // [2][128]: row scale of w and bias, bf16 each
+  float2 *cols = reinterpret_cast<float2 *>(sx + nk * C::kSxBytes);  // [2][128]: row scale of w and bias
   uint64_t *full = reinterpret_cast<uint64_t *>(cols + 2 * 128);
   uint64_t *empty = full + S;
   uint64_t *acc_full = empty + S;      // [2]
@@ -552,13 +583,13 @@ __global__ void __launch_bounds__(320, 1)
       int tl = 0;
       for (int tile = first; tile < ntiles && ok; tile += step, ++tl) {
         const int ab = tl & 1, n0 = tile * 128 + half * 64;
-        uint32_t *cw = cols + ab * 128 + half * 64;
+        float2 *cw = cols + ab * 128 + half * 64;
 #pragma unroll
         for (int c = lane; c < 64; c += 32) {
-          uint32_t col = 0x3f800000u;
+          float2 col = make_float2(1.f, 0.f);
           if (n0 + c < p.N) {
-            if (S16) col = static_cast<uint32_t>(f32_to_bf16_bits(p.rw[n0 + c])) << 16;
-            if (p.bias != nullptr) col |= p.bias[n0 + c];
+            if (S16) col.x = p.rw[n0 + c];
+            if (p.bias != nullptr) col.y = bf16_lo(p.bias[n0 + c]);
           }
           cw[c] = col;
         }
@@ -573,8 +604,8 @@ __global__ void __launch_bounds__(320, 1)
         if (lane == 0) mbar_arrive(&acc_empty[ab]);
 #pragma unroll
         for (int q = 0; q < 64; ++q) {
-          const uint32_t w = cw[q];
-          v[q] = fmaf(v[q], rx * bf16_hi(w), bf16_lo(w));
+          const float2 w = cw[q];
+          v[q] = fmaf(v[q], rx * w.x, w.y);
           if (p.gelu) v[q] = gelu_sigmoid(v[q]);
         }
         if (lane < p.T) {

@@ -390,9 +390,11 @@ CHIPMUNK_API chipmunk_status chipmunk_scatter_cols(const void *packed, int64_t n
  *               tiles of 128 rows consecutive along the columns, padded to whole
  *               256 columns (padding blocks of a row hold 0; bytes of rows past
  *               the last are not written)
- *   row_scales  [rows] fp32 (NVFP4; not used and may be NULL for MXFP4): powers of
- *               two or NaN (chipmunk_linear_fp4 takes w's rounded to bf16, which
- *               changes none of those)
+ *   row_scales  [rows] fp32 (NVFP4; not used and may be NULL for MXFP4). The quantisers
+ *               write powers of two, or NaN. Rows made elsewhere may have any scale
+ *               between 2^-110 and 2^117 (one scale of a whole tensor, repeated);
+ *               chipmunk_linear_fp4 then scales its sums with four roundings in
+ *               fp32 instead of one
  */
 #define CHIPMUNK_NVFP4 0
 #define CHIPMUNK_MXFP4 1
