@@ -669,7 +669,7 @@ def quantize_fp4_rows(x, fmt="nvfp4", out: Fp4Rows | None = None, stream=None) -
 
 
 def dequantize_fp4_rows(q: Fp4Rows, out=None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
-    """The values that 4-bit rows stand for, [R][C] in bf16 (exact) or fp32."""
+    """The values that 4-bit rows stand for, [R][C] in bf16 (exact for what ``quantize_fp4_rows`` made) or fp32."""
     lib = _lib or load_library()
     dev = q.device_index
     if out is None:

@@ -6,6 +6,7 @@
 // lane and step, so that NVFP4's row maximum costs no second pass; the block maxima
 // come from packed 16-bit maxima of the bits, and no value is divided (e2m1_grid).
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "kernels.cuh"
@@ -107,7 +108,8 @@ __device__ __forceinline__ uint2 e2m1x4_to_bf16(uint32_t c) {
 // A thread takes 16 columns of four rows at a time: per row one 8-byte code load, one scale
 // byte, one 32-byte (bf16) or four 16-byte (fp32) stores; the rows' loads go out together.
 // Every value (two code bits times four scale bits times powers of two) and the
-// scale itself are exact in bf16 within its range, so the product is taken there.
+// scale itself are exact in bf16 within its range, so the product is taken there. With a row scale that is no
+// power of two, and for fp32 output, code times block scale (exact) times row scale is rounded in fp32.
 template <int FMT, bool F32>
 __global__ void __launch_bounds__(256) dequantize_fp4_rows_kernel(const Fp4QuantParams p, void *out) {
   constexpr int R = 4;
@@ -129,34 +131,47 @@ __global__ void __launch_bounds__(256) dequantize_fp4_rows_kernel(const Fp4Quant
       sb[k] = p.scales[fp4_scale_offset(row, FMT == kNvfp4 ? g : g / 2, tiles)];
       rs[k] = FMT == kNvfp4 ? p.row_scales[row] : 1.f;
     }
+    // in_bf16: the row scales are powers of two
+    auto decode = [&](auto in_bf16) {
+      constexpr bool kInBf16 = decltype(in_bf16)::value;
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int64_t row = row0 + k * step;
-      if (row >= p.rows) break;
-      const float s = FMT == kNvfp4 ? e4m3_to_f32(sb[k]) * rs[k] : e8m0_to_f32(sb[k]);
-      const uint32_t s2 = cvt_bf16x2(s, s);
-      const uint2 h[4] = {e2m1x4_to_bf16(c[k].x & 0xffffu), e2m1x4_to_bf16(c[k].x >> 16),
-                          e2m1x4_to_bf16(c[k].y & 0xffffu), e2m1x4_to_bf16(c[k].y >> 16)};
-      uint32_t w[8];
+      for (int k = 0; k < R; ++k) {
+        const int64_t row = row0 + k * step;
+        if (row >= p.rows) break;
+        const float bs = FMT == kNvfp4 ? e4m3_to_f32(sb[k]) : e8m0_to_f32(sb[k]);
+        const uint32_t s2 = cvt_bf16x2(bs * rs[k], bs * rs[k]);
+        const uint2 h[4] = {e2m1x4_to_bf16(c[k].x & 0xffffu), e2m1x4_to_bf16(c[k].x >> 16),
+                            e2m1x4_to_bf16(c[k].y & 0xffffu), e2m1x4_to_bf16(c[k].y >> 16)};
+        uint32_t w[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = F32 ? (e & 1 ? h[e >> 1].y : h[e >> 1].x) : mul_bf16x2(e & 1 ? h[e >> 1].y : h[e >> 1].x, s2);
-      const int64_t i = row * groups + g;
-      if (F32) {
-        float4 *o = reinterpret_cast<float4 *>(out) + i * 4;
+        for (int e = 0; e < 8; ++e) {
+          w[e] = e & 1 ? h[e >> 1].y : h[e >> 1].x;
+          if (kInBf16) w[e] = mul_bf16x2(w[e], s2);
+          else if (!F32) w[e] = cvt_bf16x2(bf16_lo(w[e]) * bs * rs[k], bf16_hi(w[e]) * bs * rs[k]);
+        }
+        const int64_t i = row * groups + g;
+        if (F32) {
+          float4 *o = reinterpret_cast<float4 *>(out) + i * 4;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          o[q] = make_float4(bf16_lo(w[2 * q]) * s, bf16_hi(w[2 * q]) * s, bf16_lo(w[2 * q + 1]) * s,
-                             bf16_hi(w[2 * q + 1]) * s);
-      } else {
-        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + i * 16);
-        if (wide) {
-          store32(o, w);
+          for (int q = 0; q < 4; ++q)
+            o[q] = make_float4(bf16_lo(w[2 * q]) * bs * rs[k], bf16_hi(w[2 * q]) * bs * rs[k],
+                               bf16_lo(w[2 * q + 1]) * bs * rs[k], bf16_hi(w[2 * q + 1]) * bs * rs[k]);
         } else {
-          o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + i * 16);
+          if (wide) {
+            store32(o, w);
+          } else {
+            o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
         }
       }
-    }
+    };
+    bool powers = !F32;
+#pragma unroll
+    for (int k = 0; k < R; ++k) powers = powers && (FMT != kNvfp4 || (__float_as_uint(rs[k]) & 0x7fffffu) == 0);
+    if (powers) decode(std::true_type());
+    else decode(std::false_type());
   }
 }
 

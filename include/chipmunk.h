@@ -414,8 +414,9 @@ CHIPMUNK_API chipmunk_status chipmunk_quantize_fp4_rows(const void *x, const chi
 
 /*
  * The values q stands for, out [rows][cols] of out_type (CHIPMUNK_BF16 or
- * CHIPMUNK_FP32). They are exact in bf16, save that a value above the largest
- * finite one becomes an infinity.
+ * CHIPMUNK_FP32). With the quantisers' row scales they are exact in bf16, save that a
+ * value above the largest finite one becomes an infinity; with other row scales they are
+ * rounded to fp32, and for bf16 output once more.
  */
 CHIPMUNK_API chipmunk_status chipmunk_dequantize_fp4_rows(const chipmunk_fp4_rows *q, int32_t out_type, void *out,
                                                           chipmunk_stream stream);

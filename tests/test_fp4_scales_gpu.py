@@ -1,13 +1,26 @@
 """4-bit rows whose row scales are not the quantiser's powers of two (weights of another tool's making).
 
-Tolerance: a product scales its fp32 sums by both row scales in at most five roundings (u = 2^-24 each),
-within the 16u that (K / 64 + 8) * 2u * S grants the epilogue."""
+Tolerances: a product scales its fp32 sums by both row scales in at most five roundings (u = 2^-24 each),
+within the 16u that (K / 64 + 8) * 2u * S grants the epilogue. A value is code * block scale (exact, six bits)
+times the row scale, one rounding in fp32 (u of it) and, stored as bf16, half a step more."""
+import numpy as np
 import pytest
 
 from linear_forms import NAMES, SIZES
-from test_linear_forms_gpu import Product, cm, status_clear  # noqa: F401  (fixtures)
+from oracle import block_ops as R
+from test_linear_forms_gpu import U, Product, cm, f64, status_clear  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
+
+
+def unpacked(q):
+    packed = q.codes.cpu().numpy()
+    return np.stack([packed & 15, packed >> 4], axis=2).reshape(packed.shape[0], -1)
+
+
+def block_scales(q):
+    b = np.arange(q.cols // R.BLOCK[q.fmt])
+    return q.scales.cpu().numpy()[R.scale_offset(np.arange(q.rows)[:, None], b[None, :], q.cols, q.fmt)]
 
 
 def free_scales(q, seed=0):
@@ -18,6 +31,17 @@ def free_scales(q, seed=0):
     q.row_scales.mul_(1 + torch.rand(q.rows, generator=g, device="cuda"))
     assert float(q.row_scales.bfloat16().float().eq(q.row_scales).float().mean()) < 0.1
     return (q.row_scales.double() / old.double())[:, None]
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 32), (70, 288), (300, 1056)])
+def test_values_with_free_row_scales(cm, rows, cols):
+    import torch
+    q = cm.quantize_fp4_rows(torch.randn(rows, cols, device="cuda").bfloat16())
+    free_scales(q)
+    values = R.fp4_values(unpacked(q), block_scales(q), f64(q.row_scales), "nvfp4")
+    for dtype, allowed in ((torch.float32, U), (torch.bfloat16, 2.0 ** -8 * (1 + U) + U)):
+        d = np.abs(f64(cm.dequantize_fp4_rows(q, dtype=dtype)) - values)
+        assert np.all(d <= allowed * np.abs(values)), f"{dtype}: worst {np.max(d / np.maximum(np.abs(values), 1e-300)):.3g}"
 
 
 CASES = [(form, *sizes[0]) for form, sizes in SIZES.items()]
