@@ -25,6 +25,8 @@
 // an epilogue about 2000 more, and the chip runs it at its power cap (4.3 to 4.8 PFLOP/s sustained).
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
+#include <cmath>
 
 #include "fp4.cuh"
 #include "kernels.cuh"
@@ -44,8 +46,9 @@ struct LinCfg {
   static constexpr uint32_t kOutBytes = 4096;  // 32 rows x 128 bytes, one per epilogue warp
   static constexpr uint32_t kOutOff = kStages * kStageBytes;
   static constexpr uint32_t kColOff = kOutOff + 8 * kOutBytes;  // [BN] row scale of w and bias, bf16 each
-  static constexpr uint32_t kRatioOff = kColOff + BN * 4;       // [BN] row scale of w over its bf16
-  static constexpr uint32_t kFlagOff = kRatioOff + BN * 4;      // [8] does a warp's part of the columns have other ratios than 1
+  static constexpr uint32_t kBiasOff = kColOff + BN * 4;        // [BN] the same with row scales of 1
+  static constexpr uint32_t kScaleOff = kBiasOff + BN * 4;      // [BN] row scale of w, fp32
+  static constexpr uint32_t kFlagOff = kScaleOff + BN * 4;      // [8] warps whose columns have scales that bf16 does not hold
   static constexpr uint32_t kBarOff = kFlagOff + 32;
   static constexpr uint32_t kSmem = 1024 + kBarOff + 256;
   static constexpr uint32_t kAcc1 = BN == 256 ? 192 : BN;        // TMEM column of the second accumulator
@@ -68,6 +71,22 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int *s
 __device__ __forceinline__ float gelu_sigmoid(float u) {
   const float z2 = 1.5957691216057308f * fmaf(0.044715f * u, u * u, u);  // 2 sqrt(2/pi) (...)
   return __fdividef(u, 1.f + exp2_approx(-1.4426950408889634f * z2));
+}
+
+// A sum (at most 2^39, in steps of 2^-20) times a row scale of x and one of w. The scales' product may leave
+// fp32's range where the result does not (zero times an infinity above all). So x's scale is brought nearer to
+// one by a power of two that the sum takes up (split_scale: the scale, the sum's factor), and a product that
+// overflows all the same becomes the largest number, with which every sum but zero still overflows.
+__device__ __forceinline__ bool far_from_one(float rx) { return fabsf(rx) >= 0x1p11f || fabsf(rx) < 0x1p-30f; }
+__device__ __forceinline__ float2 split_scale(float rx) {
+  if (fabsf(rx) >= 0x1p11f) return make_float2(rx * 0x1p-24f, 0x1p24f);
+  if (fabsf(rx) < 0x1p-30f) return make_float2(rx * 0x1p40f, 0x1p-40f);
+  return make_float2(rx, 1.f);
+}
+__device__ __forceinline__ float scaled(float sum, float2 f, float rw) {
+  float m = f.x * rw;
+  if (fabsf(m) == INFINITY) m = copysignf(FLT_MAX, m);
+  return sum * f.y * m;
 }
 
 // 64 columns of this thread's TMEM lane.
@@ -251,7 +270,8 @@ __global__ void __launch_bounds__(320, 1)
     const int e = threadIdx.x - 64;
     uint8_t *stage = smem + C::kOutOff + (warp - 2) * C::kOutBytes;
     uint32_t *cols = reinterpret_cast<uint32_t *>(smem + C::kColOff);
-    float *ratios = reinterpret_cast<float *>(smem + C::kRatioOff);
+    uint32_t *biases = reinterpret_cast<uint32_t *>(smem + C::kBiasOff);
+    float *scales = reinterpret_cast<float *>(smem + C::kScaleOff);
     uint32_t *flags = reinterpret_cast<uint32_t *>(smem + C::kFlagOff);
     int tl = 0;
     wait_for_primary();  // the row scales of x
@@ -271,37 +291,36 @@ __global__ void __launch_bounds__(320, 1)
       const int ab = tl & 1;
       const int row0 = (mt * CG + rank) * 128 + quad * 32;
       // this row's factor; this thread's column: row scale of w above, bias below, both bf16, which holds
-      // the quantiser's powers of two and NaN; for other scales a ratio makes up for it
-      const float rx = S16 && row0 + lane < p.T ? p.rx[row0 + lane] : 1.f;
+      // the quantiser's powers of two and NaN
+      float rx = S16 && row0 + lane < p.T ? p.rx[row0 + lane] : 1.f;
       const int n = nt * BN + e;
-      float ratio = 1.f;
-      uint32_t col = 0x3f800000u;
+      float rw = 1.f;
+      uint32_t bias = 0;
       if (e < BN && n < p.N) {
-        if (S16) {
-          const float rw = p.rw[n];
-          const uint32_t hi = f32_to_bf16_bits(rw);
-          col = hi << 16;
-          if ((__float_as_uint(rw) & 0xffffu) != 0) ratio = __fdiv_rn(rw, bf16_lo(hi));
-        }
-        if (p.bias != nullptr) col |= p.bias[n];
+        if (S16) rw = p.rw[n];
+        if (p.bias != nullptr) bias = p.bias[n];
       }
-      const bool odd = S16 && __any_sync(0xffffffffu, ratio != 1.f);
+      const bool odd = S16 && __any_sync(0xffffffffu, (__float_as_uint(rw) & 0xffffu) != 0);
       // the warps have read the previous tile's column values; put this tile's in place
       if (lane == 0) mbar_arrive(col_bar);
       if (!wait_warp(col_bar, 0, p.status, abort_flag)) break;
       if (e < BN) {
-        cols[e] = col;
-        if (S16) ratios[e] = ratio;
+        cols[e] = bias | static_cast<uint32_t>(f32_to_bf16_bits(rw)) << 16;
+        if (S16) biases[e] = bias | 0x3f800000u, scales[e] = rw;
       }
       if (S16 && lane == 0) flags[warp - 2] = odd;
       __syncwarp();
       if (lane == 0) mbar_arrive(col_bar);
       if (!wait_warp(col_bar, 1, p.status, abort_flag)) break;
-      bool odd_scales = false;  // the same for all warps
+      // in a tile with other scales, and in a warp with scales far from one, both are applied ahead of the rest
+      bool ahead = false;
       if (S16) {
         const uint4 f0 = reinterpret_cast<const uint4 *>(flags)[0], f1 = reinterpret_cast<const uint4 *>(flags)[1];
-        odd_scales = (f0.x | f0.y | f0.z | f0.w | f1.x | f1.y | f1.z | f1.w) != 0;
+        ahead = (f0.x | f0.y | f0.z | f0.w | f1.x | f1.y | f1.z | f1.w) != 0 || __any_sync(0xffffffffu, far_from_one(rx));
       }
+      const uint32_t *colp = ahead ? biases : cols;
+      const float rxs = rx;
+      if (ahead) rx = 1.f;
       if (!wait_warp(&acc_full[ab], (tl >> 1) & 1, p.status, abort_flag)) break;
       tc_fence_after();
       // The columns both accumulators share are the last 64 of the first one and the
@@ -313,14 +332,15 @@ __global__ void __launch_bounds__(320, 1)
         tmem_ld64(tmem + ab * C::kAcc1 + (static_cast<uint32_t>(quad * 32) << 16) + c0, v);
         if (has_shared && i == 0) release(shared_empty);
         if (i == kChunks - 1) release(&acc_empty[ab]);
-        // The part of w's row scales that the bf16 below does not hold: two roundings more (ratio and product), in
-        // tiles with such scales only, where it takes 79 instead of 64 us at 12000 x 9216 x 256, 51 instead of
-        // 46 at 4352 x 12288 x 1024, and is hidden behind the MMAs at longer sums.
-        if (S16 && odd_scales) {
+        // Two roundings more, where the scales need it only: 86 instead of 63 us at 12000 x 9216 x 256, 55
+        // instead of 46 at 4352 x 12288 x 1024, 56.5 instead of 52.5 at 4352 x 9216 x 3072.
+        if (S16 && ahead) {
+          const float2 f = split_scale(rxs);
 #pragma unroll
           for (int q = 0; q < 64; q += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(ratios + c0 + q);
-            v[q] *= f.x, v[q + 1] *= f.y, v[q + 2] *= f.z, v[q + 3] *= f.w;
+            const float4 w = *reinterpret_cast<const float4 *>(scales + c0 + q);
+            v[q] = scaled(v[q], f, w.x), v[q + 1] = scaled(v[q + 1], f, w.y);
+            v[q + 2] = scaled(v[q + 2], f, w.z), v[q + 3] = scaled(v[q + 3], f, w.w);
           }
         }
         // Every lane reads every column's values, a shared-memory wavefront for each
@@ -329,7 +349,7 @@ __global__ void __launch_bounds__(320, 1)
         for (int g = 0; g < 64; g += 16) {
           uint4 w[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const uint4 *>(cols + c0 + g + 4 * q);
+          for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const uint4 *>(colp + c0 + g + 4 * q);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const uint32_t w0 = q & 1 ? w[q >> 1].z : w[q >> 1].x, w1 = q & 1 ? w[q >> 1].w : w[q >> 1].y;
@@ -580,6 +600,8 @@ __global__ void __launch_bounds__(320, 1)
       const int half = warp >> 3;
       bool ok = wait_warp(x_ready, 0, p.status, abort_flag);
       const float rx = S16 && lane < p.T ? nvfp4_row_scale(row_max[lane & 7]) : 1.f;
+      const float2 f = split_scale(rx);
+      const bool far = __any_sync(0xffffffffu, far_from_one(rx));
       int tl = 0;
       for (int tile = first; tile < ntiles && ok; tile += step, ++tl) {
         const int ab = tl & 1, n0 = tile * 128 + half * 64;
@@ -605,7 +627,7 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
         for (int q = 0; q < 64; ++q) {
           const float2 w = cw[q];
-          v[q] = fmaf(v[q], rx * w.x, w.y);
+          v[q] = far ? scaled(v[q], f, w.x) + w.y : fmaf(v[q], rx * w.x, w.y);
           if (p.gelu) v[q] = gelu_sigmoid(v[q]);
         }
         if (lane < p.T) {

@@ -393,8 +393,8 @@ CHIPMUNK_API chipmunk_status chipmunk_scatter_cols(const void *packed, int64_t n
  *   row_scales  [rows] fp32 (NVFP4; not used and may be NULL for MXFP4). The quantisers
  *               write powers of two, or NaN. Rows made elsewhere may have any scale
  *               between 2^-110 and 2^117 (one scale of a whole tensor, repeated);
- *               chipmunk_linear_fp4 then scales its sums with four roundings in
- *               fp32 instead of one
+ *               chipmunk_linear_fp4 then rounds three times in fp32 where it scales its
+ *               sums, instead of once
  */
 #define CHIPMUNK_NVFP4 0
 #define CHIPMUNK_MXFP4 1

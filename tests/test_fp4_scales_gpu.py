@@ -70,3 +70,52 @@ def test_products_with_free_row_scales(cm, form, T, N, K):
     fx = free_scales(p.xq, 1)
     p.sums, p.mag = p.sums * fx, p.mag * fx
     p.check(out_dtype=torch.float32, quantised=True)
+
+
+def check_range(got, ref, slack):
+    """Finite where the definition is clear of the type's largest number, an infinity of its sign where it is beyond."""
+    import torch
+    stored, step = (2.0 ** -8, 2.0 ** -133) if got.dtype == torch.bfloat16 else (U, 2.0 ** -149)
+    got, top = got.double(), float(torch.finfo(torch.bfloat16).max)
+    inside, beyond = ref.abs() + slack < top * (1 - 2.0 ** -7), ref.abs() - slack > 2.0 ** 128
+    d = (got - ref).abs()[inside] - (stored * ref.abs() + slack + step)[inside]
+    assert bool(got[inside].isfinite().all()) and float(d.max()) <= 0
+    assert torch.equal(got[beyond], torch.sign(ref[beyond]) * float("inf"))
+    assert not bool(got.isnan().any())
+    return inside, beyond
+
+
+@pytest.mark.parametrize("form,T,N,K", CASES, ids=[NAMES[c[0]] for c in CASES])
+def test_row_scales_far_from_one(cm, form, T, N, K):
+    """Rows of x and w from 2^-100 to 2^100: the product of two row scales leaves fp32's range both ways."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(form)
+    e = lambda n: torch.randint(-5, 6, (n, 1), generator=g, device="cuda") * 20
+    ex, ew = e(T), e(N)
+    x = (torch.randn(T, K, generator=g, device="cuda") * torch.exp2(ex.float())).bfloat16()
+    w = (torch.randn(N, K, generator=g, device="cuda") * torch.exp2(ew.float())).bfloat16()
+    x[:, K // 2:] = 0
+    w[::5, :K // 2] = 0                      # sums of nothing but zeros
+    wq, xq = cm.quantize_fp4_rows(w), cm.quantize_fp4_rows(x)
+    xv, wv = (cm.dequantize_fp4_rows(q, dtype=torch.float32).double() for q in (xq, wq))
+    ref, S = xv @ wv.t(), xv.abs() @ wv.abs().t()
+    for dtype in (torch.float32, torch.bfloat16):
+        out = cm.linear_fp4(x, wq, out_dtype=dtype)
+        inside, beyond = check_range(out, ref, (K / 64 + 8) * 2 * U * S)
+        assert bool(beyond.any()) and not bool(out[:, ::5].any())
+    bias = torch.randn(N, generator=g, device="cuda").bfloat16()
+    out = cm.linear_fp4(xq, wq, bias, out_dtype=torch.float32)
+    check_range(out, ref + bias.double(), (K / 64 + 8) * 2 * U * (S + bias.double().abs()))
+
+
+def test_small_products_are_not_lost(cm):
+    """Both operands small: sums of 4096 equal terms land where fp32 still holds them, their scales' product not."""
+    import torch
+    for T in (2, 40):
+        x = torch.full((T, 4096), 2.0 ** -95, device="cuda").bfloat16()
+        w = cm.quantize_fp4_rows(torch.full((136, 4096), 2.0 ** -40, device="cuda").bfloat16())
+        for a in (x, cm.quantize_fp4_rows(x)):
+            out = cm.linear_fp4(a, w, out_dtype=torch.float32).double()
+            v = cm.dequantize_fp4_rows(cm.quantize_fp4_rows(x), dtype=torch.float32).double()
+            ref = v @ cm.dequantize_fp4_rows(w, dtype=torch.float32).double().t()
+            check_range(out.float(), ref, (4096 / 64 + 8) * 2 * U * ref)
