@@ -185,9 +185,11 @@ void launch_w(const Fp4QuantParams &p, cudaStream_t s) {
   const int rows = W == 1 ? 4 : 1;
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((p.rows + rows - 1) / rows, 148 * (W == 16 ? 4 : 16)));
   const unsigned threads = W == 1 ? 128 : 32 * W;
-  if (need <= 1) quantize_fp4_rows_kernel<FMT, W, 1><<<blocks, threads, 0, s>>>(p);
-  else if (need <= 2) quantize_fp4_rows_kernel<FMT, W, 2><<<blocks, threads, 0, s>>>(p);
-  else if (need <= 4) quantize_fp4_rows_kernel<FMT, W, 4><<<blocks, threads, 0, s>>>(p);
+  if constexpr (W == 1) {  // more warps hold a row of more than two steps only
+    if (need <= 1) return quantize_fp4_rows_kernel<FMT, W, 1><<<blocks, threads, 0, s>>>(p);
+    if (need <= 2) return quantize_fp4_rows_kernel<FMT, W, 2><<<blocks, threads, 0, s>>>(p);
+  }
+  if (need <= 4) quantize_fp4_rows_kernel<FMT, W, 4><<<blocks, threads, 0, s>>>(p);
   else if (need <= 6) quantize_fp4_rows_kernel<FMT, W, 6><<<blocks, threads, 0, s>>>(p);
   else quantize_fp4_rows_kernel<FMT, W, 8><<<blocks, threads, 0, s>>>(p);
 }

@@ -18,7 +18,6 @@
 // per thread; column group v * G + t belongs to thread t, so every access is 16
 // bytes per lane and consecutive over a warp.
 #include <algorithm>
-#include <type_traits>
 
 #include "fp4.cuh"
 #include "kernels.cuh"
@@ -428,21 +427,21 @@ void launch_types(const NormParams &p, cudaStream_t s) {
 // The kernel takes all but a thread's last column group for granted: each width goes to
 // the form whose groups it fills but for the last.
 //
-// Without y: up to three column groups per thread (four at the largest widths).
+// Without y: two or three column groups per thread (one at the smallest widths, four at the largest).
 template <bool R32>
 void launch_plain(const NormParams &p, cudaStream_t s) {
   const int ng = p.D / 8;
-  auto by_nv = [&](auto w) {
-    constexpr int W = decltype(w)::value;
-    if (ng <= 32 * W) launch_types<W, 1, R32, kYNone>(p, s);
-    else if (ng <= 64 * W) launch_types<W, 2, R32, kYNone>(p, s);
-    else launch_types<W, 3, R32, kYNone>(p, s);
-  };
-  if (ng <= 96) by_nv(std::integral_constant<int, 1>());
-  else if (ng <= 192) by_nv(std::integral_constant<int, 2>());
-  else if (ng <= 384) by_nv(std::integral_constant<int, 4>());
-  else if (ng <= 768) by_nv(std::integral_constant<int, 8>());
-  else if (ng <= 1536) by_nv(std::integral_constant<int, 16>());
+  if (ng <= 32) launch_types<1, 1, R32, kYNone>(p, s);
+  else if (ng <= 64) launch_types<1, 2, R32, kYNone>(p, s);
+  else if (ng <= 96) launch_types<1, 3, R32, kYNone>(p, s);
+  else if (ng <= 128) launch_types<2, 2, R32, kYNone>(p, s);
+  else if (ng <= 192) launch_types<2, 3, R32, kYNone>(p, s);
+  else if (ng <= 256) launch_types<4, 2, R32, kYNone>(p, s);
+  else if (ng <= 384) launch_types<4, 3, R32, kYNone>(p, s);
+  else if (ng <= 512) launch_types<8, 2, R32, kYNone>(p, s);
+  else if (ng <= 768) launch_types<8, 3, R32, kYNone>(p, s);
+  else if (ng <= 1024) launch_types<16, 2, R32, kYNone>(p, s);
+  else if (ng <= 1536) launch_types<16, 3, R32, kYNone>(p, s);
   else launch_types<16, 4, R32, kYNone>(p, s);
 }
 

@@ -126,14 +126,6 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, ui
       : "memory");
 }
 
-// `bytes` consecutive bytes global -> shared (both 16-byte aligned, a multiple of 16).
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 // Tile shared -> global. Parts of the tile past the tensor's ends are dropped.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *tm, const void *src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(

@@ -78,10 +78,6 @@ def fp4_values(codes, sb, rs, fmt):
     return (mag.reshape(R, -1, BLOCK[fmt]) * step[:, :, None]).reshape(R, C)
 
 
-def pack_codes(codes):
-    return (codes[:, 0::2] | codes[:, 1::2] << 4).astype(np.uint8)
-
-
 def scale_offset(r, b, C, fmt):
     """Byte of the scale of row r, block b."""
     tiles = -(-C // 256) * (256 // BLOCK[fmt] // 4)
