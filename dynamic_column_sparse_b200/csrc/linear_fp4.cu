@@ -6,8 +6,8 @@
 // Persistent, one CTA per SM. Three forms: a CTA pair (cta_group::2) on a 256 x
 // 256 output tile, each CTA holding 128 rows of x, 128 rows of w and 128 rows of
 // the result; and one CTA on a 128 x 256 or 128 x 128 tile where larger tiles would leave SMs
-// idle (linear_fp4_form chooses; a fourth form, below, takes a few rows). Tiles are walked weight-slice fastest, so a row block of x is read
-// from HBM once while the weights stay in L2.
+// idle (linear_fp4_form chooses; a fourth form, below, takes a few rows). Tiles are walked weight-slice
+// fastest, so a row block of x is read from HBM once while the weights stay in L2.
 //
 // Warp 0 fills a ring of stages of 256 columns with TMA: code tiles
 // (128-byte swizzle) and the block scales' 512-byte tiles. Warp 1 (of the leading CTA)
@@ -67,7 +67,8 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int *s
 }
 
 // GELU, tanh form, as u * sigmoid(2 z) by the identity (1 + tanh z) / 2 =
-// 1 / (1 + e^(-2z)); relative error a few 2^-22.
+// 1 / (1 + e^(-2z)). The error is a few 2^-22 of |u|. Relative to the result it grows in the negative tail, where
+// the exponent's rounding (a few 2^-24 of 2 |z|) is the result's: to about 2^-15 at 2 |z| = 87, the last fp32 holds.
 __device__ __forceinline__ float gelu_sigmoid(float u) {
   const float z2 = 1.5957691216057308f * fmaf(0.044715f * u, u * u, u);  // 2 sqrt(2/pi) (...)
   return __fdividef(u, 1.f + exp2_approx(-1.4426950408889634f * z2));
@@ -601,7 +602,7 @@ __global__ void __launch_bounds__(320, 1)
       bool ok = wait_warp(x_ready, 0, p.status, abort_flag);
       const float rx = S16 && lane < p.T ? nvfp4_row_scale(row_max[lane & 7]) : 1.f;
       const float2 f = split_scale(rx);
-      const bool far = __any_sync(0xffffffffu, far_from_one(rx));
+      const bool far = S16 && __any_sync(0xffffffffu, far_from_one(rx));
       int tl = 0;
       for (int tile = first; tile < ntiles && ok; tile += step, ++tl) {
         const int ab = tl & 1, n0 = tile * 128 + half * 64;
@@ -624,11 +625,16 @@ __global__ void __launch_bounds__(320, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_empty[ab]);
+        if (far) {
 #pragma unroll
-        for (int q = 0; q < 64; ++q) {
-          const float2 w = cw[q];
-          v[q] = far ? scaled(v[q], f, w.x) + w.y : fmaf(v[q], rx * w.x, w.y);
-          if (p.gelu) v[q] = gelu_sigmoid(v[q]);
+          for (int q = 0; q < 64; ++q) v[q] = scaled(v[q], f, cw[q].x) + cw[q].y;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 64; ++q) v[q] = fmaf(v[q], rx * cw[q].x, cw[q].y);
+        }
+        if (p.gelu) {
+#pragma unroll
+          for (int q = 0; q < 64; ++q) v[q] = gelu_sigmoid(v[q]);
         }
         if (lane < p.T) {
           const int64_t o = static_cast<int64_t>(lane) * p.N + n0;
@@ -723,7 +729,8 @@ cudaError_t launch_linear_fp4(const LinearFp4Params &p, const LinearFp4Maps &m, 
 // call costs the host 5 us less; at 8 rows of 3072 the quantiser in every CTA would take 2.5 us
 // more than its own launch. Otherwise the form of
 // the least estimated time on 148 SMs: waves x (time of a tile's ends + time of its
-// K / 256 stages), in units of 10 ns, fitted to measurements of NVFP4 products (us):
+// K / 256 stages), in units of 10 ns, fitted to measurements of NVFP4 products (MXFP4 goes by them too). It takes the
+// shortest of each row but one: 1024 x 3072 x 3072 runs as pairs, 4% longer than wide tiles would (us):
 //                            single    wide     pair
 //     333 x 12288 x 3072       13.7    12.6     16.4
 //    1024 x  3072 x 3072       12.2    10.4     10.8

@@ -244,10 +244,14 @@ __device__ __forceinline__ void write_fp4(const uint4 (&h)[NV], const uint32_t (
 // CTAs per SM that the registers are held to (80 a thread, 64 with one column group, 128
 // with four); the grid is one wave of them, so that every CTA walks its rows with the next
 // one in flight. Measured at 20000 rows of 3072 columns: without y four warps of three column groups
-// (45.8 us; with 96 registers 47.8, with 72 and spills 57.7; six warps of two 55.9), with y six warps of
+// (45.8 us; with 96 registers 47.8, with 72 and larger spills 57.7; six warps of two 55.9), with y six warps of
 // two (80.8 us in bf16, 119.5 with an fp32 residual; four warps of three 93 and 139). With y and quantised
-// output four warps of three would take 86.4 instead of 101 us, but the sums' order, and with it
+// output four warps of three would take 86.4 instead of 98 us, but the sums' order, and with it
 // some last bits, would then differ between the output formats.
+// The budgets were chosen at that width and hold for all. There the bf16 forms spill nothing, the fp32 one without y 68
+// bytes a thread; others spill up to 136 bytes, and 20 to 248 above 8192 columns, where one CTA of 16 warps is all that an
+// SM holds. Over the time of the bytes at the copy rate, 61 M values, gated bf16 (fp32 without y): 1536 columns 1.13
+// (1.06), 3072 1.09 (1.04), 5120 1.23 (1.35), 8192 1.31 (1.40), 10240 1.48 (1.49), 16384 1.66 (1.59).
 constexpr int ctas_per_sm(int W, int NV, bool r32, int y) {
   const int regs = NV == 4 || (NV == 3 && W == 16 && y != 0) ? 128 : NV == 1 || (NV == 2 && y == 0 && !r32) ? 64 : 80;
   const int n = 65536 / (32 * (W == 1 ? 4 : W) * regs);

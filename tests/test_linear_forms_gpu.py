@@ -170,3 +170,18 @@ def test_large_forms_in_a_graph_and_on_two_streams(cm, form):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(ref, outs))
+
+
+@pytest.mark.parametrize("T", [1, 40], ids=["rows", "single"])
+def test_gelu_over_its_range(cm, T):
+    """Products of zero rows are the bias, exactly: GELU alone. With 2z the exponent (within 7u of its value in
+    fp32), the result's relative error is at most 2 |z| 7u, and 2^-20 for exp2, the sum and the division."""
+    import torch
+    u = torch.linspace(-9.5, 9.5, 4096, device="cuda").bfloat16()
+    w = cm.quantize_fp4_rows(torch.ones(u.numel(), 32, device="cuda").bfloat16())
+    x = torch.zeros(T, 32, device="cuda").bfloat16()
+    got = cm.linear_fp4(x, w, u, act="gelu", out_dtype=torch.float32).double()
+    u = u.double()
+    z2 = 2 * math.sqrt(2 / math.pi) * (u + 0.044715 * u ** 3)
+    ref = (u / (1 + torch.exp(-z2))).expand(T, -1)
+    assert bool(((got - ref).abs() <= (z2.abs() * 7 * U + 2.0 ** -20) * ref.abs()).all())
