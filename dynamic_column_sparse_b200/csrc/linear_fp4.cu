@@ -725,7 +725,7 @@ cudaError_t launch_linear_fp4(const LinearFp4Params &p, const LinearFp4Maps &m, 
 }
 
 // A few rows of bf16 x are quantised in the product's kernel (kRowItems per thread at most): 1
-// x 18432 x 3072 takes 10.5 us in one launch, 12.9 us in two, 1 x 3072 x 3072 9.1 against 8.6 us, and a
+// x 18432 x 3072 takes 8.5 us in a graph, 1 x 3072 x 3072 8.2 (two launches 12.9 and 8.6), and a
 // call costs the host 5 us less; at 8 rows of 3072 the quantiser in every CTA would take 2.5 us
 // more than its own launch. Otherwise the form of
 // the least estimated time on 148 SMs: waves x (time of a tile's ends + time of its
