@@ -109,7 +109,8 @@ __device__ __forceinline__ uint2 e2m1x4_to_bf16(uint32_t c) {
 // byte, one 32-byte (bf16) or four 16-byte (fp32) stores; the rows' loads go out together.
 // Every value (two code bits times four scale bits times powers of two) and the
 // scale itself are exact in bf16 within its range, so the product is taken there. With a row scale that is no
-// power of two, and for fp32 output, code times block scale (exact) times row scale is rounded in fp32.
+// power of two, and for fp32 output, code times block scale (exact) times row scale is rounded in fp32
+// (4352 x 12288 to bf16: 27 us instead of 24.5; one loop for both kinds of row took 26 for either).
 template <int FMT, bool F32>
 __global__ void __launch_bounds__(256) dequantize_fp4_rows_kernel(const Fp4QuantParams p, void *out) {
   constexpr int R = 4;
